@@ -75,6 +75,10 @@ def lib():
                                            P]
     L.qlora_linear_bwd_fmt.argtypes = [P, P, P, i32, i32, i64, i64, P, P, i64, P, P, i32, f32, P, P, P, P, P, sz,
                                        P]
+    L.qlora_head_workspace.argtypes = [i64, i64, i64, i32, i32, i32, i64, P]
+    L.qlora_head_xent.argtypes = [P, P, P, P, i32, i32, i64, i64, P, i64, P, P, P, P, P, P, sz, P]
+    L.qlora_head_distill.argtypes = [P, P, P, P, i32, i32, i64, i64, P, i64, P, P, i32, i32, f32, P, P, P, P, P, sz,
+                                     P]
     L.qlora_device_status.restype = i32
     L.qlora_test_decode_timeout.argtypes = [P, P, P, i64, i64, P, i64, P, P, i32, f32, P, P, sz, P]
     L.qlora_trace_gemm_events.argtypes = [P, i32]
@@ -430,6 +434,106 @@ def qlora_linear_fwd_noalloc(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: 
                                           _ptr(A), _ptr(B), r, float(scale), _ptr(out), _ptr(H), _stream(stream)),
            "qlora_linear_fwd_noalloc")
     return out, H
+
+
+def head_workspace_bytes(M, N, K, k=0, want_dx=True, nf4=False, piece=0) -> int:
+    """Workspace bytes of qlora_head_xent (k = 0) or qlora_head_distill (k teacher
+    slots per token); piece: tokens taken at once (0: the library's choice)."""
+    b = ctypes.c_size_t()
+    _check(lib().qlora_head_workspace(M, N, K, k, int(want_dx), int(nf4), piece, ctypes.byref(b)),
+           "qlora_head_workspace")
+    return b.value
+
+
+def _head_call(fn, what, head, X, k, targets, dloss, outs, workspace, stream):
+    """The checks, allocations and call that the two head losses share.
+    targets: the (tensor, dtype, name, shape) checks and the arguments between M
+    and dloss."""
+    if isinstance(head, NF4Weight):
+        N, K = head.N, head.K
+        buffers = [head.codes, head.absmax_q, head.dq_scale]
+        weight = (None, _ptr(head.codes), _ptr(head.absmax_q) if head.absmax_q.numel() else None,
+                  _ptr(head.dq_scale), head.block, head.dq_block)
+    else:
+        _req(head, torch.bfloat16, "head")
+        if head.dim() != 2:
+            raise ValueError(f"head must have shape (N, K), got {tuple(head.shape)}")
+        N, K = head.shape
+        buffers = [head]
+        weight = (_ptr(head), None, None, None, BLOCK, DQ_BLOCK)
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a tensor of shape (M, K)")
+    M = X.shape[0]
+    _req(X, torch.bfloat16, "X", (M, K))
+    checks, args = targets(M)
+    for t, dtype, name, shape in checks:
+        _req(t, dtype, name, shape)
+    if dloss is not None:
+        _req(dloss, torch.float32, "dloss", (M,))
+    dev = X.device
+    loss, lse, dX = outs if outs is not None else (None, None, None)
+    for t, dtype, name, shape in ((loss, torch.float32, "loss", (M,)), (lse, torch.float32, "lse", (M,)),
+                                  (dX, torch.bfloat16, "dX", (M, K))):
+        if t is not None:
+            _req(t, dtype, name, shape)
+    if dX is not None and dloss is None:
+        raise ValueError("dX is given but dloss is not")
+    every = buffers + [c[0] for c in checks] + [t for t in (dloss, loss, lse, dX, workspace) if t is not None]
+    if any(t.device != dev for t in every):
+        raise ValueError("all tensors must be on the device of X")
+    if stream is not None and stream.device != dev:
+        raise ValueError("stream must belong to the device of X")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):  # allocations belong to the stream that uses them
+        if loss is None:
+            loss = torch.empty(M, dtype=torch.float32, device=dev)
+        if lse is None:
+            lse = torch.empty(M, dtype=torch.float32, device=dev)
+        if dX is None and dloss is not None:
+            dX = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = torch.empty(head_workspace_bytes(M, N, K, k, dX is not None, isinstance(head, NF4Weight)),
+                                    dtype=torch.uint8, device=dev)
+        _check(fn(*weight, N, K, _ptr(X), M, *args, _ptr(dloss), _ptr(loss), _ptr(lse), _ptr(dX), _ptr(workspace),
+                  workspace.numel() * workspace.element_size(), _stream()), what)
+    return loss, lse, dX
+
+
+def qlora_head_xent(head, X: torch.Tensor, labels: torch.Tensor, dloss: torch.Tensor | None = None, outs=None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Softmax cross entropy through a frozen output head, without storing the
+    logits Z = X head^T.  head: bf16 [N, K] or an NF4Weight; labels: int64 [M],
+    entries outside [0, N) leave the token out.  Returns (loss, lse, dX): fp32
+    [M] each, and with dloss (fp32 [M], the objective's gradient with respect to
+    each loss) dX = dloss (softmax(Z) - onehot(labels)) head in bf16, else None.
+    outs: (loss, lse, dX) tensors to write, any of them None."""
+    def targets(M):
+        return [(labels, torch.int64, "labels", (M,))], (_ptr(labels),)
+
+    return _head_call(lib().qlora_head_xent, "qlora_head_xent", head, X, 0, targets, dloss, outs, workspace, stream)
+
+
+def qlora_head_distill(head, X: torch.Tensor, teacher_idx: torch.Tensor, teacher_logits: torch.Tensor,
+                       temperature: float = 1.0, dloss: torch.Tensor | None = None, outs=None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Distillation through a frozen output head from a teacher's k kept logits:
+    loss = T^2 KL(softmax(teacher_logits / T) || softmax(Z / T)) with the
+    teacher's distribution over its kept slots.  teacher_idx: int64 [M, k]
+    (outside [0, N): an empty slot); teacher_logits: fp32 or bf16 [M, k].
+    Returns (loss, lse, dX) as qlora_head_xent, lse being that of Z / T."""
+    if not isinstance(teacher_idx, torch.Tensor) or teacher_idx.dim() != 2:
+        raise ValueError("teacher_idx must be a tensor of shape (M, k)")
+    k = teacher_idx.shape[1]
+    if not isinstance(teacher_logits, torch.Tensor) or teacher_logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("teacher_logits must be a torch.float32 or torch.bfloat16 tensor")
+
+    def targets(M):
+        return ([(teacher_idx, torch.int64, "teacher_idx", (M, k)),
+                 (teacher_logits, teacher_logits.dtype, "teacher_logits", (M, k))],
+                (_ptr(teacher_idx), _ptr(teacher_logits), int(teacher_logits.dtype == torch.bfloat16), k,
+                 float(temperature)))
+
+    return _head_call(lib().qlora_head_distill, "qlora_head_distill", head, X, k, targets, dloss, outs, workspace,
+                      stream)
 
 
 def gemm_resident_pairs(mode: int = 0) -> int:

@@ -252,6 +252,67 @@ int check_format(int64_t K, int block, int dq_block) {
   return K % block ? QLORA_ERR_SHAPE : QLORA_OK;
 }
 
+namespace {
+
+// Shape rules of the head losses: K % 64 == 0 (as the layer), any N >= 1, at
+// most QLORA_HEAD_MAX_TARGETS teacher slots per token (k = 0: cross entropy).
+int check_head_shapes(int64_t M, int64_t N, int64_t K, int k) {
+  if (M < 0 || N <= 0 || K <= 0) return QLORA_ERR_ARG;
+  if (k > QLORA_HEAD_MAX_TARGETS) return QLORA_ERR_UNSUPPORTED;
+  if (K % 64) return QLORA_ERR_SHAPE;
+  if (M > (1 << 24) || N > (1 << 24) || K > (1 << 20) || N * K > (int64_t(1) << 40)) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+// The checks and the launch that the two head losses share (`a` holds what is
+// theirs alone).
+int run_head(HeadArgs& a, const uint16_t* W, const uint8_t* codes, const uint8_t* absmax_q, const float* dq_scale,
+             int block, int dq_block, int64_t N, int64_t K, const uint16_t* X, int64_t M, const float* dloss,
+             float* loss, float* lse, uint16_t* dX, void* workspace, size_t workspace_bytes, void* stream) {
+  const bool distill = a.labels == nullptr && a.teacher_idx != nullptr;
+  int st = check_head_shapes(M, N, K, distill ? a.k : 0);
+  if (st) return st;
+  if ((W != nullptr) == (codes != nullptr)) return QLORA_ERR_ARG;  // exactly one kind of head
+  if (codes) {
+    st = check_format(K, block, dq_block);
+    if (st) return st;
+    if ((dq_block && !absmax_q) || !dq_scale) return QLORA_ERR_ARG;
+  }
+  if (M == 0) return QLORA_OK;
+  if (!X || !loss || !lse || (dloss && !dX)) return QLORA_ERR_ARG;
+  const void* ptrs[] = {W, codes, X, dX};
+  for (const void* p : ptrs)
+    if (p && !aligned(p, 16)) return QLORA_ERR_SHAPE;
+  const void* words[] = {a.labels, a.teacher_idx};
+  for (const void* p : words)
+    if (p && !aligned(p, 8)) return QLORA_ERR_SHAPE;
+  const void* floats[] = {dloss, loss, lse, dq_scale, a.teacher_bf16 ? nullptr : a.teacher_logits};
+  for (const void* p : floats)
+    if (p && !aligned(p, 4)) return QLORA_ERR_SHAPE;
+  if (a.teacher_bf16 && !aligned(a.teacher_logits, 2)) return QLORA_ERR_SHAPE;
+  a.W = W;
+  a.codes = codes;
+  a.absmax_q = absmax_q;
+  a.dq_scale = dq_scale;
+  a.block = block;
+  a.dq_block = dq_block;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.X = X;
+  a.dloss = dloss;
+  a.loss = loss;
+  a.lse = lse;
+  a.dX = dX;
+  a.workspace = workspace;
+  if (!workspace || !aligned(workspace, 256)) return QLORA_ERR_WORKSPACE;
+  a.piece = head_piece(workspace_bytes, M, N, K, a.k, distill, dX != nullptr, codes != nullptr);
+  if (a.piece <= 0) return QLORA_ERR_WORKSPACE;
+  return cuda_status(launch_head_loss(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
 int* device_status_ptr() { return symbol_ptr(g_status_ptr, &g_device_status); }
 int* device_nonfinite_ptr() { return symbol_ptr(g_nonfinite_ptr, &g_nonfinite); }
 
@@ -788,6 +849,44 @@ int qlora_test_decode_timeout(const uint8_t* codes, const uint8_t* absmax_q, con
   cudaError_t e = launch_rowdot(X, A, M, K, r, scale, w.Hs, 1.0f, nullptr, nullptr, s);
   if (e == cudaSuccess) e = launch_gemv(X, M, codes, absmax_q, dq_scale, N, K, w.Hs, B, r, Y, s, nullptr, 0, true);
   return cuda_status(e);
+}
+
+int qlora_head_workspace(int64_t M, int64_t N, int64_t K, int k, int want_dx, int nf4, int64_t piece,
+                         size_t* bytes) {
+  if (!bytes || k < 0 || piece < 0) return QLORA_ERR_ARG;
+  const int st = check_head_shapes(M, N, K, k);
+  if (st) return st;
+  *bytes = head_workspace_bytes(piece, M, N, K, k > 0 ? k : 1, k > 0, want_dx != 0, nf4 != 0);
+  return QLORA_OK;
+}
+
+int qlora_head_xent(const qlora_bf16_t* W, const uint8_t* codes, const uint8_t* absmax_q, const float* dq_scale,
+                    int block, int dq_block, int64_t N, int64_t K, const qlora_bf16_t* X, int64_t M,
+                    const int64_t* labels, const float* dloss, float* loss, float* lse, qlora_bf16_t* dX,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  HeadArgs a;
+  a.labels = labels;
+  if (M > 0 && !labels) return QLORA_ERR_ARG;
+  return run_head(a, W, codes, absmax_q, dq_scale, block, dq_block, N, K, X, M, dloss, loss, lse, dX, workspace,
+                  workspace_bytes, stream);
+}
+
+int qlora_head_distill(const qlora_bf16_t* W, const uint8_t* codes, const uint8_t* absmax_q, const float* dq_scale,
+                       int block, int dq_block, int64_t N, int64_t K, const qlora_bf16_t* X, int64_t M,
+                       const int64_t* teacher_idx, const void* teacher_logits, int teacher_bf16, int k,
+                       float temperature, const float* dloss, float* loss, float* lse, qlora_bf16_t* dX,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (k < 1) return QLORA_ERR_ARG;
+  if (M > 0 && (!teacher_idx || !teacher_logits)) return QLORA_ERR_ARG;
+  if (!(temperature >= 1e-4f && temperature <= 1e4f)) return QLORA_ERR_ARG;
+  HeadArgs a;
+  a.teacher_idx = teacher_idx;
+  a.teacher_logits = teacher_logits;
+  a.teacher_bf16 = teacher_bf16 != 0;
+  a.k = k;
+  a.temperature = temperature;
+  return run_head(a, W, codes, absmax_q, dq_scale, block, dq_block, N, K, X, M, dloss, loss, lse, dX, workspace,
+                  workspace_bytes, stream);
 }
 
 int qlora_device_status(void) {

@@ -1,0 +1,872 @@
+// The head losses: softmax cross entropy and distillation from a teacher's top
+// logits, through a frozen output head W [N, K] (N = vocabulary, K = hidden
+// width), with the gradient of the head's input X [M, K].
+//
+//   z = X W^T / T,  lse_i = log sum_j exp z_ij,  p_ij = exp(z_ij - lse_i)
+//   loss_i = T^2 sum_s q_is (log q_is - (z_i,idx(s) - lse_i))
+//   dX_i   = dloss_i T (sum_j p_ij w_j - sum_s q_is w_idx(s))
+// with one target per row (q = 1, T = 1) for cross entropy, and the softmax of
+// the teacher's kept logits over T for distillation.
+//
+// The logits never reach memory.  A product kernel (k_head<0>) leaves, for each
+// row and each tile of the vocabulary, the tile's maximum and its sum of
+// exponentials, and the target logits it meets, all in fp32 straight from the
+// accumulator; k_head_stats joins them into lse and loss.  For the gradient the
+// same kernel also writes e = exp(z - tile maximum) in bf16 for a piece of the
+// tokens; once lse is known, k_head_scale turns e into p - q in place (one
+// multiplication by exp(tile maximum - lse); the target columns are computed
+// from their fp32 logits, because p - 1 from a rounded p would be noise for a
+// confident token), and k_head<1> multiplies by W again.  So a loss with its
+// gradient costs two products; computing p from the logits a second time would
+// need three, and keeping the logits themselves in bf16 would cost accuracy:
+// a rounding error of 2^-9 of a logit near 20 is 4 % of its p, while the same
+// rounding of e is 2^-9 of p.
+#include <algorithm>
+#include <atomic>
+
+#include "internal.h"
+
+namespace qn {
+
+namespace {
+
+constexpr int UM = 128;      // token rows of each CTA of a pair
+constexpr int TM = 2 * UM;   // token rows of a tile
+constexpr int TN = 256;      // largest tile width (vocabulary entries or outputs)
+constexpr int BK = 64;       // contraction per stage
+constexpr int STAGES = 6;
+constexpr int A_BYTES = UM * BK * 2;
+constexpr int B_BYTES = TN / 2 * BK * 2;
+constexpr int OFF_B = STAGES * A_BYTES;
+constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
+constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignment
+constexpr int EPI_WARPS = 4;
+constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
+constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
+constexpr int kNoTarget = 0x7fffffff;
+
+static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+
+struct HeadBars {
+  uint64_t full[STAGES];   // this CTA's tiles landed
+  uint64_t peer[STAGES];   // leader: the peer's tiles landed
+  uint64_t empty[STAGES];  // MMAs of the stage completed (multicast by the leader)
+  uint64_t acc_full[2];    // accumulator complete (multicast by the leader)
+  uint64_t acc_empty[2];   // leader: both CTAs' epilogue warps have read it
+  uint64_t drain;          // leader: used only when aborting
+  uint64_t dealloc;        // the other CTA finished with the pair's TMEM
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(HeadBars) <= 256, "barrier block");
+
+// Work items: whole tiles, then nsplit pieces (of the contraction) of each of
+// the last ntail tiles, as in the fused NF4 GEMM.
+struct HeadGrid {
+  int mtiles, ntiles;         // token tiles of 256, output tiles of bn
+  int nwhole, ntail, nsplit;
+  int band;                   // token tiles walked together
+  int bn;                     // outputs per tile (a multiple of 32; 256 for MODE 1)
+};
+
+__device__ __forceinline__ void tile_of(const HeadGrid& g, int L, int& mt, int& nt) {
+  const int per_band = g.band * g.ntiles;
+  const int b = L / per_band, rem = L - b * per_band;
+  const int in_band = min(g.band, g.mtiles - b * g.band);
+  nt = rem / in_band;
+  mt = b * g.band + (rem - nt * in_band);
+}
+
+// exp2 on the special-function unit: relative error about 2^-22, which is far
+// below the bf16 rounding of e and of the order of the fp32 sums' own rounding.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t tmem_ld_one(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return r;
+}
+
+// What the epilogues read and write (MODE 0: logits, MODE 1: gradient).
+struct HeadEpi {
+  int rows;         // token rows of the piece
+  int cols;         // MODE 0: N; MODE 1: K
+  // MODE 0
+  float c;                   // log2(e) / T
+  float2* part;              // [ntiles][rows]: (maximum * c, sum of exp2(z c - maximum c))
+  uint16_t* e;               // [rows][lde] (nullable)
+  int64_t lde;
+  const int64_t* labels;     // [rows] (cross entropy), or
+  const int* sidx;           // [rows][k] targets in ascending order, and
+  const uint16_t* off;       // [rows][ntiles + 1] first target of each tile
+  int k;
+  float* ztgt;               // [rows][k] target logits (times c)
+  // MODE 1
+  const float* rscale;       // [rows] factor of the row (0: the row is written as zeros)
+  uint16_t* out;             // [rows][cols]
+  float* split;              // fp32 sums of the split tiles' pieces
+};
+
+// D = A B^T by pairs of CTAs (cta_group::2): 256 tokens x up to 256 outputs per
+// tile, each CTA holding 128 token rows and half of the output rows of each
+// stage, both brought by TMA.  MODE 0: A = X, B = W (K-major).  MODE 1: A = p - q
+// [rows, N], B = W with its rows as the contraction (MN-major).
+//
+// A persistent pair walks its items; two accumulators of 256 TMEM columns let
+// the epilogue of one tile run under the products of the next.
+//   warp 0     TMA producer
+//   warp 1     TMEM allocation; the leader issues the MMAs, the peer reports its
+//              landed stages to the leader
+//   warps 2-5  epilogue, one TMEM lane quarter each: a thread owns a token row
+// Every wait is bounded; on expiry the kernel records kDevTimeout, drains what
+// it issued, frees TMEM and returns.
+template <int MODE>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    k_head(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int numK, HeadGrid g,
+           HeadEpi p, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  HeadBars* bars = reinterpret_cast<HeadBars*>(smem_raw + (base - raw) + OFF_BAR);
+  const uint32_t bar0 = base + OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto peer = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto acc_full = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
+  auto acc_empty = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  const uint32_t dealloc_bar = drain_bar + 8u;
+  volatile int* abort = &bars->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0 = leader, 1 = peer
+  const bool leader = rank == 0;
+  const int bnl = g.bn >> 1;
+  const int nitems = g.nwhole + g.ntail * g.nsplit;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  // Item i: its tile, and the stages [kbeg, kend) of the contraction it covers.
+  auto item = [&](int i, int& mt, int& nt, int& kbeg, int& kend, int& tail, int& z) {
+    int L = i;
+    tail = -1;
+    z = 0;
+    kbeg = 0;
+    kend = numK;
+    if (i >= g.nwhole) {
+      const int j = i - g.nwhole;
+      tail = j / g.nsplit;
+      z = j - tail * g.nsplit;
+      L = g.nwhole + tail;
+      kbeg = static_cast<int>(static_cast<int64_t>(z) * numK / g.nsplit);
+      kend = static_cast<int>(static_cast<int64_t>(z + 1) * numK / g.nsplit);
+    }
+    tile_of(g, L, mt, nt);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(peer(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(acc_full(a), 1);
+      mbar_init(acc_empty(a), 2 * EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    mbar_init(dealloc_bar, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(bar0 + static_cast<uint32_t>(offsetof(HeadBars, tmem_base)), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0) {
+    // --------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      const uint32_t bytes = A_BYTES + static_cast<uint32_t>(bnl) * BK * 2;
+      bool ok = true;
+      int n = 0;  // stages issued
+      for (int i = first; i < nitems && ok; i += step) {
+        int mt, nt, kbeg, kend, tail, z;
+        item(i, mt, nt, kbeg, kend, tail, z);
+        const int m0 = mt * TM + static_cast<int>(rank) * UM, n0 = nt * g.bn + static_cast<int>(rank) * bnl;
+        for (int k = kbeg; k < kend; ++k) {
+          const int s = n % STAGES;
+          if (!(ok = wait_bounded(empty(s), ((n / STAGES) & 1) ^ 1, abort, status))) break;
+          mbar_arrive_expect_tx(full(s), bytes);
+          tma_load_2d(base + s * A_BYTES, &tm_a, full(s), k * BK, m0);
+          const uint32_t b_s = base + OFF_B + s * B_BYTES;
+          if (MODE == 0) {
+            tma_load_2d(b_s, &tm_b, full(s), k * BK, n0);
+          } else {
+            tma_load_2d(b_s, &tm_b, full(s), n0, k * BK);
+            tma_load_2d(b_s + 8192, &tm_b, full(s), n0 + 64, k * BK);
+          }
+          ++n;
+        }
+      }
+      if (!ok)  // let the copies already issued land before the CTA exits
+        for (int i = (n > STAGES ? n - STAGES : 0); i < n; ++i) wait_drain(full(i % STAGES), (i / STAGES) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------- MMA issuer (leader), relay (peer)
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(TM, g.bn, false, MODE == 1);
+      const uint32_t peer_at_leader = mapa_shared(peer(0), 0);
+      bool ok = true, committed = false;
+      int n = 0, t = 0;  // stages and tiles so far
+      for (int i = first; i < nitems && ok; i += step, ++t) {
+        int mt, nt, kbeg, kend, tail, z;
+        item(i, mt, nt, kbeg, kend, tail, z);
+        const uint32_t d = tmem + 256u * (t & 1);
+        if (leader) {
+          if (!(ok = wait_bounded_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
+          tc_fence_after();
+        }
+        for (int k = kbeg; k < kend; ++k, ++n) {
+          const int s = n % STAGES;
+          const uint32_t ph = (n / STAGES) & 1;
+          if (!(ok = wait_bounded(full(s), ph, abort, status))) break;
+          if (!leader) {
+            mbar_arrive_remote(peer_at_leader + 8u * s);
+            continue;
+          }
+          if (!(ok = wait_bounded_cluster(peer(s), ph, abort, status))) break;
+          tc_fence_after();
+          const uint32_t a_s = base + s * A_BYTES, b_s = base + OFF_B + s * B_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t bd =
+                MODE == 0 ? desc_sw128(b_s + kk * 32, 16, 1024) : desc_sw128(b_s + kk * 2048, 8192, 1024);
+            tc_mma_f16_pair(d, desc_sw128(a_s + kk * 32, 16, 1024), bd, idesc, (k > kbeg || kk > 0) ? 1u : 0u);
+          }
+          tc_commit_pair(empty(s));
+          committed = true;
+        }
+        if (leader && ok) tc_commit_pair(acc_full(t & 1));
+      }
+      if (!ok && committed) {  // wait for MMAs in flight before TMEM is freed
+        tc_commit_pair(drain_bar);
+        wait_drain(drain_bar, 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    const int quad = warp & 3;  // TMEM lanes 32 quad .. 32 quad + 31
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t empty_at_leader = mapa_shared(acc_empty(0), 0);
+    int t = 0;
+    for (int i = first; i < nitems; i += step, ++t) {
+      int mt, nt, kbeg, kend, tail, z;
+      item(i, mt, nt, kbeg, kend, tail, z);
+      const int row0 = mt * TM + static_cast<int>(rank) * UM + quad * 32;  // the warp's first row
+      const int row = row0 + lane;
+      const int n0 = nt * g.bn;
+      const bool landed = wait_bounded(acc_full(t & 1), (t >> 1) & 1, abort, status);
+      if (!__all_sync(0xffffffffu, landed)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + lane_base + 256u * (t & 1);
+      if (MODE == 0 && row0 < p.rows) {
+        const bool live = row < p.rows;
+        const int ncols = min(g.bn, p.cols - n0);
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int col = 0; col < ncols; col += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + col, v);
+          tmem_ld_wait();
+          if (col + 32 <= ncols) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j < ncols) mx = fmaxf(mx, __uint_as_float(v[j]));
+          }
+        }
+        // The tile's reference in units of log2: kept as rounded here, so that
+        // sum * exp2(reference) does not depend on that rounding.
+        // (A tile whose logits are all -inf or NaN is summed around 0.)
+        const float ref = mx == -INFINITY ? 0.0f : __fmul_rn(mx, p.c);
+        float sum = 0.0f;
+        uint16_t* erow = p.e ? p.e + static_cast<int64_t>(row) * p.lde + n0 : nullptr;
+        const int ewidth = static_cast<int>(min(static_cast<int64_t>(g.bn), p.lde - n0));
+#pragma unroll 1
+        for (int col = 0; col < ewidth; col += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + col, v);
+          tmem_ld_wait();
+          float e[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), p.c, -ref));
+            if (col + 32 > ncols && col + j >= ncols) e[j] = 0.0f;
+          }
+          if (p.e && live) {
+            uint4* dst = reinterpret_cast<uint4*>(erow + col);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(bf16x2_bits(e[8 * q], e[8 * q + 1]), bf16x2_bits(e[8 * q + 2], e[8 * q + 3]),
+                                  bf16x2_bits(e[8 * q + 4], e[8 * q + 5]), bf16x2_bits(e[8 * q + 6], e[8 * q + 7]));
+          }
+          // As a tree: a column with p near 1 then meets the small rest in 13
+          // additions per tile, not in one for each of them (a loss of 1e-5 is
+          // the difference of the sum from 1).
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < d; ++j) e[j] += e[j + d];
+          sum += e[0];
+        }
+        if (live)
+          p.part[static_cast<int64_t>(nt) * p.rows + row] =
+              make_float2(mx == -INFINITY ? mx : ref, sum);
+        // Target logits: the warp visits the columns that any of its rows wants,
+        // in ascending order (at most bn of them, usually none or a few).
+        int cur = 0, end = 0, want = kNoTarget;
+        if (live) {
+          if (p.labels) {
+            const int64_t y = p.labels[row];
+            if (y >= n0 && y < n0 + ncols) {
+              want = static_cast<int>(y);
+              end = 1;
+            }
+          } else {
+            const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.ntiles + 1) + nt;
+            cur = o[0];
+            end = o[1];
+            if (cur < end) want = p.sidx[static_cast<int64_t>(row) * p.k + cur];
+          }
+        }
+        for (;;) {
+          const int c = __reduce_min_sync(0xffffffffu, want);
+          if (c == kNoTarget) break;
+          const uint32_t v = tmem_ld_one(acc + (c - n0));
+          tmem_ld_wait();
+          if (want == c) {
+            p.ztgt[static_cast<int64_t>(row) * p.k + cur] = __uint_as_float(v) * p.c;
+            ++cur;
+            want = cur < end ? p.sidx[static_cast<int64_t>(row) * p.k + cur] : kNoTarget;
+          }
+        }
+      }
+      if (MODE == 1 && row0 < p.rows) {
+        const bool live = row < p.rows;
+        const float f = live && tail < 0 ? p.rscale[row] : 0.0f;
+#pragma unroll 1
+        for (int col = 0; col < TN && n0 + col < p.cols; col += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + col, v);
+          tmem_ld_wait();
+          if (tail >= 0) {  // a piece of a split tile: fp32 sums, joined by k_head_join
+            float4* dst = reinterpret_cast<float4*>(
+                p.split + ((static_cast<int64_t>(tail) * g.nsplit + z) * TM + rank * UM + quad * 32 + lane) * TN + col);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+          } else if (live) {
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = f == 0.0f ? 0.0f : __uint_as_float(v[j]) * f;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n0 + col);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)  // cols % 64 == 0: a group of 32 columns is whole
+              dst[q] = make_uint4(bf16x2_bits(x[8 * q], x[8 * q + 1]), bf16x2_bits(x[8 * q + 2], x[8 * q + 3]),
+                                  bf16x2_bits(x[8 * q + 4], x[8 * q + 5]), bf16x2_bits(x[8 * q + 6], x[8 * q + 7]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(acc_empty(t & 1));
+        else mbar_arrive_remote(empty_at_leader + 8u * (t & 1));
+      }
+    }
+  }
+
+  // Both CTAs must be done with the pair's TMEM, and with each other's
+  // barriers, before either leaves: each tells the other and waits (bounded).
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) {
+      mbar_arrive_remote(mapa_shared(dealloc_bar, rank ^ 1u));
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait_cluster(dealloc_bar, 0)) {
+        if (global_timer_ns() - t0 > 2 * kWaitLimitNs) {
+          atomicExch(status, kDevTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// Sum of the pieces of the split gradient tiles in piece order, times the row's
+// factor, rounded once to bf16.  Thread: 8 consecutive outputs of a row.
+__global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ split, HeadGrid g, HeadEpi p) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  constexpr int per_tile = TM * (TN / 8);
+  const int t = static_cast<int>(i / per_tile), w = static_cast<int>(i % per_tile);
+  if (t >= g.ntail) return;
+  const int r = w / (TN / 8), c = (w % (TN / 8)) * 8;
+  int mt, nt;
+  tile_of(g, g.nwhole + t, mt, nt);
+  const int row = mt * TM + r, n = nt * TN + c;
+  if (row >= p.rows || n >= p.cols) return;
+  const float* src = split + (static_cast<int64_t>(t) * g.nsplit * TM + r) * TN + c;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+  for (int z = 0; z < g.nsplit; ++z) {
+    const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
+    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    src += TM * TN;
+  }
+  const float f = p.rscale[row];
+  uint4 o = make_uint4(0u, 0u, 0u, 0u);
+  if (f != 0.0f)
+    o = make_uint4(bf16x2_bits(a.x * f, a.y * f), bf16x2_bits(a.z * f, a.w * f), bf16x2_bits(b.x * f, b.y * f),
+                   bf16x2_bits(b.z * f, b.w * f));
+  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n) = o;
+}
+
+// The teacher's slots of one row per block: the softmax of the kept logits over
+// T (as logarithms), in ascending order of their vocabulary index (ties in slot
+// order), and where each vocabulary tile's targets begin.  A slot whose index
+// is outside [0, N) or whose logit is -inf holds nothing: it sorts last.  k is
+// at most 256, so each thread ranks its slot by comparing it with the others.
+template <typename T>
+__global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict__ idx, const T* __restrict__ logit,
+                                                      int k, int N, float inv_t, int bn, int ntiles,
+                                                      int* __restrict__ sidx, float* __restrict__ logq,
+                                                      uint16_t* __restrict__ off) {
+  __shared__ int key[256], sorted[256];
+  __shared__ float val[256];
+  const int64_t row = blockIdx.x;
+  const int s = threadIdx.x;
+  for (int j = s; j < k; j += blockDim.x) {
+    const int64_t y = idx[row * k + j];
+    const float x = static_cast<float>(logit[row * k + j]) * inv_t;
+    const bool kept = y >= 0 && y < N && x != -INFINITY;
+    key[j] = kept ? static_cast<int>(y) : kNoTarget;
+    val[j] = x;
+  }
+  __syncthreads();
+  float mx = -INFINITY, sum = 0.0f;
+  for (int j = 0; j < k; ++j)
+    if (key[j] != kNoTarget) mx = fmaxf(mx, val[j]);
+  for (int j = 0; j < k; ++j)
+    if (key[j] != kNoTarget) sum += expf(val[j] - mx);
+  const float lsum = logf(sum);
+  for (int j = s; j < k; j += blockDim.x) {
+    const int mine = key[j];
+    int rank = 0;
+    for (int o = 0; o < k; ++o) rank += (key[o] < mine || (key[o] == mine && o < j)) ? 1 : 0;
+    sorted[rank] = mine;
+    sidx[row * k + rank] = mine;
+    logq[row * k + rank] = mine == kNoTarget ? -INFINITY : (val[j] - mx) - lsum;
+  }
+  __syncthreads();
+  for (int t = s; t <= ntiles; t += blockDim.x) {
+    const int64_t bound = min(static_cast<int64_t>(t) * bn, static_cast<int64_t>(N));
+    int lo = 0, hi = k;  // first slot with sorted >= bound
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sorted[mid] < bound) lo = mid + 1;
+      else hi = mid;
+    }
+    off[row * (ntiles + 1) + t] = static_cast<uint16_t>(lo);
+  }
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Factor that takes a sum of exponentials from reference x to reference top.
+__device__ __forceinline__ float shift2(float x, float top) { return x == -INFINITY ? 0.0f : exp2f(x - top); }
+
+// Joins the tiles' (reference, sum) pairs of 32 rows per block: first thread
+// (r, j) takes row r and tiles j, j + 32, ..., then warp r joins its row's 32
+// values and adds up its targets.  The orders are fixed.
+__global__ void __launch_bounds__(1024)
+    k_head_stats(const float2* __restrict__ part, int ntiles, int rows, int N, const int64_t* __restrict__ labels,
+                 const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float* __restrict__ ztgt,
+                 float temp, const float* __restrict__ dloss, float* __restrict__ loss, float* __restrict__ lse,
+                 float2* __restrict__ lse2, float* __restrict__ rscale) {
+  __shared__ float2 sh[32][33];
+  const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
+  const int row0 = blockIdx.x * 32;
+  float m = -INFINITY, s = 0.0f;
+  if (row0 + a < rows) {
+    for (int t = b; t < ntiles; t += 32) {
+      const float2 v = part[static_cast<int64_t>(t) * rows + row0 + a];
+      const float top = fmaxf(m, v.x);
+      s = s * shift2(m, top) + v.y * shift2(v.x, top);
+      m = top;
+    }
+  }
+  sh[b][a] = make_float2(m, s);
+  __syncthreads();
+  const int row = row0 + b;
+  if (row >= rows) return;
+  const float2 v = sh[a][b];
+  m = v.x;
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  s = v.y * shift2(v.x, m);
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  const float l2s = log2f(s);
+  // loss = T^2 sum_s q_s (log q_s + (lse - z_s)); lse - z_s in units of log2 is
+  // (reference - z_s) + log2(sum), which keeps the digits of a small loss.
+  float part_loss = 0.0f;
+  bool any = false;
+  if (labels) {
+    const int64_t y = labels[row];
+    any = y >= 0 && y < N;
+    if (any && a == 0) part_loss = ((m - ztgt[row]) + l2s) * kLn2;
+  } else {
+    const int64_t at = static_cast<int64_t>(row) * k;
+    any = sidx[at] != kNoTarget;
+    for (int j = a; j < k; j += 32) {
+      if (sidx[at + j] == kNoTarget) break;
+      const float lq = logq[at + j], q = expf(lq);
+      if (q != 0.0f) part_loss += q * (lq + ((m - ztgt[at + j]) + l2s) * kLn2);
+    }
+  }
+  for (int d = 16; d > 0; d >>= 1) part_loss += __shfl_xor_sync(0xffffffffu, part_loss, d);
+  if (a == 0) {
+    loss[row] = any ? part_loss * (temp * temp) : 0.0f;
+    lse[row] = (m + l2s) * kLn2;
+    if (rscale) {
+      lse2[row] = make_float2(m, l2s);
+      rscale[row] = any ? (dloss ? dloss[row] : 1.0f) * temp : 0.0f;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
+  return bf16x2_bits(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+}
+
+// e -> p - q in place, one block per row: p = e exp2(reference - lse), rounded
+// to bf16 again; target columns hold exp(z - lse) - q from their fp32 logits
+// (cross entropy: expm1, exact where p is near 1).
+__global__ void __launch_bounds__(256)
+    k_head_scale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int bn, int rows, int N,
+                 const float2* __restrict__ lse2, const float* __restrict__ rscale, const int64_t* __restrict__ labels,
+                 const int* __restrict__ sidx, const float* __restrict__ logq, int k,
+                 const float* __restrict__ ztgt) {
+  const int row = blockIdx.x;
+  if (rscale[row] == 0.0f) return;  // its gradient is written as zeros
+  const float2 l2 = lse2[row];  // subtracted in two steps: their sum would round off digits of z - lse
+  uint16_t* er = e + static_cast<int64_t>(row) * lde;
+  uint4* v = reinterpret_cast<uint4*>(er);
+  const int chunks = static_cast<int>(lde / 8), per_tile = bn / 8;
+  for (int c = threadIdx.x; c < chunks; c += 256) {
+    const float f = exp2f(part[static_cast<int64_t>(c / per_tile) * rows + row].x - l2.x - l2.y);
+    uint4 x = v[c];
+    x.x = scale_pair(x.x, f);
+    x.y = scale_pair(x.y, f);
+    x.z = scale_pair(x.z, f);
+    x.w = scale_pair(x.w, f);
+    v[c] = x;
+  }
+  __syncthreads();
+  if (labels) {
+    if (threadIdx.x == 0) {
+      const float d = expm1f((ztgt[row] - l2.x - l2.y) * kLn2);
+      er[labels[row]] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
+    }
+  } else {
+    const int64_t at = static_cast<int64_t>(row) * k;
+    for (int j = threadIdx.x; j < k; j += 256) {
+      const int y = sidx[at + j];
+      if (y == kNoTarget || (j > 0 && sidx[at + j - 1] == y)) continue;
+      float d = exp2f(ztgt[at + j] - l2.x - l2.y);
+      for (int o = j; o < k && sidx[at + o] == y; ++o) d -= expf(logq[at + o]);
+      er[y] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
+    }
+  }
+}
+
+// ------------------------------------------------------------ host side
+
+cudaLaunchConfig_t pair_config(int pairs, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_ALLOC;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Pairs of CTAs resident at once on the current device (0: unknown).
+int head_pairs() {
+  constexpr int kDev = 64;
+  static std::atomic<int> cache[kDev];  // 0: not yet asked; -1: unknown
+  int d = -1;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kDev) {
+    cudaGetLastError();
+    return 0;
+  }
+  int v = cache[d].load(std::memory_order_relaxed);
+  if (v == 0) {
+    cudaLaunchAttribute attr[1];
+    int a = 0, b = 0;
+    const cudaLaunchConfig_t cfg = pair_config(1, nullptr, attr);
+    if (smem_limit_once<k_head<0>>(SMEM_ALLOC) == cudaSuccess &&
+        smem_limit_once<k_head<1>>(SMEM_ALLOC) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&a, k_head<0>, &cfg) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&b, k_head<1>, &cfg) == cudaSuccess && std::min(a, b) > 0) {
+      v = std::min(a, b);
+    } else {
+      cudaGetLastError();
+      v = -1;
+    }
+    cache[d].store(v, std::memory_order_relaxed);
+  }
+  return v > 0 ? v : 0;
+}
+
+// Token tiles walked together: their A rows (256 rows of the contraction each)
+// stay near 48 MB, so they stay in L2 while the other operand streams past.
+int band_of(int64_t mtiles, int64_t contraction) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(mtiles, (48ll << 20) / (TM * contraction * 2))));
+}
+
+// Tiles of the logits product.
+HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
+  HeadGrid g{};
+  g.mtiles = static_cast<int>((rows + TM - 1) / TM);
+  g.bn = TN;
+  g.ntiles = static_cast<int>((N + g.bn - 1) / g.bn);
+  g.nwhole = g.mtiles * g.ntiles;
+  g.nsplit = 1;
+  g.band = band_of(g.mtiles, K);
+  return g;
+}
+
+// Tiles of the gradient product; the tiles of a partial last wave are split
+// along the vocabulary.
+HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
+  HeadGrid g{};
+  g.mtiles = static_cast<int>((rows + TM - 1) / TM);
+  g.bn = TN;
+  g.ntiles = static_cast<int>((K + TN - 1) / TN);
+  g.nwhole = g.mtiles * g.ntiles;
+  g.nsplit = 1;
+  g.band = g.mtiles;
+  const int64_t numK = (N + BK - 1) / BK;
+  const int P = head_pairs();
+  if (P <= 0) return g;
+  const int64_t w = g.nwhole % P;
+  if (w == 0) return g;
+  int64_t S = 1;
+  double best = 0.0;
+  for (int64_t c = 2; c <= std::min<int64_t>(numK / 8, 64); ++c) {
+    const double rounds = static_cast<double>((w * c + P - 1) / P);
+    const double save = (1.0 - rounds / static_cast<double>(c)) * static_cast<double>(numK) - 0.1 * w * c;
+    if (save > best) {
+      best = save;
+      S = c;
+    }
+  }
+  if (S > 1) {
+    g.nsplit = static_cast<int>(S);
+    g.ntail = static_cast<int>(w);
+    g.nwhole -= g.ntail;
+  }
+  return g;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Workspace of a call of M tokens whose pieces hold `rows` (the last one M % rows).
+struct HeadSpace {
+  uint16_t* w16;
+  float2* part;
+  float2* lse2;  // [rows]: log2 of the sum of exponentials as (largest reference, log2 of the sum relative to it)
+  float *ztgt, *logq, *rscale, *split;
+  int* sidx;
+  uint16_t *off, *e;
+  size_t bytes;
+};
+int64_t e_pitch(int64_t N) { return (N + 63) / 64 * 64; }
+
+HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad, bool nf4) {
+  HeadSpace s{};
+  size_t at = 0;
+  auto take = [&](size_t n) -> void* {
+    uint8_t* q = ws ? static_cast<uint8_t*>(ws) + at : nullptr;
+    at += up256(n);
+    return q;
+  };
+  const HeadGrid g = logits_grid(rows, N, K);
+  if (nf4) s.w16 = static_cast<uint16_t*>(take(static_cast<size_t>(N) * K * 2));
+  s.part = static_cast<float2*>(take(static_cast<size_t>(g.ntiles) * rows * 8));
+  s.ztgt = static_cast<float*>(take(static_cast<size_t>(rows) * k * 4));
+  if (distill) {
+    s.sidx = static_cast<int*>(take(static_cast<size_t>(rows) * k * 4));
+    s.logq = static_cast<float*>(take(static_cast<size_t>(rows) * k * 4));
+    s.off = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * (g.ntiles + 1) * 2));
+  }
+  if (grad) {
+    s.lse2 = static_cast<float2*>(take(static_cast<size_t>(rows) * 8));
+    s.rscale = static_cast<float*>(take(static_cast<size_t>(rows) * 4));
+    s.e = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * e_pitch(N) * 2));
+    const HeadGrid d = grad_grid(rows, N, K), last = grad_grid(M % rows, N, K);
+    const int64_t pieces = std::max(int64_t(d.ntail) * d.nsplit, int64_t(last.ntail) * last.nsplit);
+    s.split = static_cast<float*>(take(static_cast<size_t>(pieces) * TM * TN * 4));
+  }
+  s.bytes = at;
+  return s;
+}
+
+// Tokens per piece when the caller leaves the choice to the library: with a
+// gradient e takes at most 512 MB, without one the tiles' statistics are small
+// and 16384 tokens go at once.  Pieces of a call are alike, in whole tiles.
+int64_t default_piece(int64_t M, int64_t N, bool grad) {
+  const int64_t most =
+      grad ? std::max<int64_t>(TM, (512ll << 20) / (e_pitch(N) * 2) / TM * TM) : int64_t(64) * TM;
+  const int64_t pieces = std::max<int64_t>(1, (M + most - 1) / most);
+  return std::max<int64_t>(1, std::min<int64_t>(M, ((M + pieces - 1) / pieces + TM - 1) / TM * TM));
+}
+
+template <int MODE>
+cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, int64_t contraction, const HeadGrid& g,
+                        const HeadEpi& p, cudaStream_t st) {
+  cudaError_t e = smem_limit_once<k_head<MODE>>(SMEM_ALLOC);
+  if (e != cudaSuccess) return e;
+  const int64_t items = int64_t(g.nwhole) + int64_t(g.ntail) * g.nsplit;
+  int P = head_pairs();
+  if (P <= 0) P = std::max(1, device_sm_count() / 2);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pair_config(static_cast<int>(std::min<int64_t>(items, P)), st, attr);
+  return cudaLaunchKernelEx(&cfg, k_head<MODE>, a, b, static_cast<int>((contraction + BK - 1) / BK), g, p,
+                            device_status_ptr());
+}
+
+}  // namespace
+
+size_t head_workspace_bytes(int64_t piece, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad,
+                            bool nf4) {
+  const int64_t rows = piece > 0 ? std::min(piece, std::max<int64_t>(M, 1)) : default_piece(M, N, grad);
+  return std::max<size_t>(256, head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes);
+}
+
+int64_t head_piece(size_t bytes, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad, bool nf4) {
+  int64_t rows = default_piece(M, N, grad);
+  while (head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes > bytes) {
+    if (rows <= TM) return 0;
+    rows = ((rows + 1) / 2 + TM - 1) / TM * TM;
+  }
+  return rows;
+}
+
+cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
+  const bool distill = a.labels == nullptr, grad = a.dX != nullptr, nf4 = a.W == nullptr;
+  const HeadSpace s = head_space(a.workspace, a.piece, a.M, a.N, a.K, a.k, distill, grad, nf4);
+  const auto BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B;
+  cudaError_t err = cudaSuccess;
+  const uint16_t* W = a.W;
+  if (nf4) {
+    err = launch_dequantize(a.codes, a.absmax_q, a.dq_scale, a.N * a.K, a.block, a.dq_block, s.w16, st);
+    if (err != cudaSuccess) return err;
+    W = s.w16;
+  }
+  const int64_t lde = e_pitch(a.N);
+  for (int64_t r0 = 0; r0 < a.M; r0 += a.piece) {
+    const int64_t rows = std::min(a.piece, a.M - r0);
+    const HeadGrid g = logits_grid(rows, a.N, a.K);
+    const uint16_t* X = a.X + r0 * a.K;
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, BF16, X, a.K, rows, a.K * 2, BK, UM, SW) ||
+        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, BK, g.bn / 2, SW))
+      return cudaErrorInvalidValue;
+    HeadEpi p{};
+    p.rows = static_cast<int>(rows);
+    p.cols = static_cast<int>(a.N);
+    p.c = 1.4426950408889634f / a.temperature;
+    p.part = s.part;
+    p.e = s.e;
+    p.lde = lde;
+    p.labels = distill ? nullptr : a.labels + r0;
+    p.sidx = s.sidx;
+    p.off = s.off;
+    p.k = a.k;
+    p.ztgt = s.ztgt;
+    if (distill) {
+      const dim3 grid(static_cast<unsigned>(rows)), block(std::max(128, (a.k + 31) / 32 * 32));
+      const int64_t* idx = a.teacher_idx + r0 * a.k;
+      const float inv_t = 1.0f / a.temperature;
+      if (a.teacher_bf16)
+        err = launch_ex(k_head_targets<__nv_bfloat16>, grid, block, 0, st, false, idx,
+                        static_cast<const __nv_bfloat16*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.bn,
+                        g.ntiles, s.sidx, s.logq, s.off);
+      else
+        err = launch_ex(k_head_targets<float>, grid, block, 0, st, false, idx,
+                        static_cast<const float*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.bn, g.ntiles,
+                        s.sidx, s.logq, s.off);
+      if (err != cudaSuccess) return err;
+    }
+    err = launch_head<0>(ma, mb, a.K, g, p, st);
+    if (err != cudaSuccess) return err;
+    err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(1024), 0, st, false,
+                    static_cast<const float2*>(s.part), g.ntiles, p.rows, p.cols, p.labels,
+                    static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
+                    static_cast<const float*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
+                    a.lse + r0, s.lse2, s.rscale);
+    if (err != cudaSuccess || !grad) {
+      if (err != cudaSuccess) return err;
+      continue;
+    }
+    err = launch_ex(k_head_scale, dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, false, s.e, lde,
+                    static_cast<const float2*>(s.part), g.bn, p.rows, p.cols, static_cast<const float2*>(s.lse2),
+                    static_cast<const float*>(s.rscale), p.labels, static_cast<const int*>(s.sidx),
+                    static_cast<const float*>(s.logq), a.k, static_cast<const float*>(s.ztgt));
+    if (err != cudaSuccess) return err;
+    const HeadGrid d = grad_grid(rows, a.N, a.K);
+    if (!make_map(&ma, BF16, s.e, lde, rows, lde * 2, BK, UM, SW) ||
+        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, 64, BK, SW))
+      return cudaErrorInvalidValue;
+    HeadEpi q{};
+    q.rows = p.rows;
+    q.cols = static_cast<int>(a.K);
+    q.rscale = s.rscale;
+    q.out = a.dX + r0 * a.K;
+    q.split = s.split;
+    err = launch_head<1>(ma, mb, a.N, d, q, st);
+    if (err == cudaSuccess && d.ntail)
+      err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (TN / 8) / 256))), dim3(256), 0, st,
+                      false, static_cast<const float*>(s.split), d, q);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace qn

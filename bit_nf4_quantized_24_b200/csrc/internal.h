@@ -146,6 +146,34 @@ cudaError_t launch_dx_add_masked(uint16_t* dX, const uint16_t* dH, const uint16_
 cudaError_t launch_rows_multi(const uint16_t* X, int64_t M, int64_t K, const uint16_t* A_all, int na, int r,
                               const float* scales, const int32_t* aidx, uint16_t* Hs, cudaStream_t st);
 
+// ----- head losses (cross entropy, distillation) through a frozen head W [N, K]
+struct HeadArgs {
+  const uint16_t* W = nullptr;  // bf16 [N, K]; null: the NF4 weight below
+  const uint8_t* codes = nullptr;
+  const uint8_t* absmax_q = nullptr;
+  const float* dq_scale = nullptr;
+  int block = 64, dq_block = 256;
+  int64_t M = 0, N = 0, K = 0;
+  const uint16_t* X = nullptr;
+  const int64_t* labels = nullptr;       // cross entropy: [M]; null: distillation
+  const int64_t* teacher_idx = nullptr;  // [M, k]
+  const void* teacher_logits = nullptr;  // [M, k] fp32 or bf16
+  bool teacher_bf16 = false;
+  int k = 1;  // targets per token (1 for cross entropy)
+  float temperature = 1.0f;
+  const float* dloss = nullptr;  // [M] (null: ones)
+  float* loss = nullptr;
+  float* lse = nullptr;
+  uint16_t* dX = nullptr;  // null: no gradient
+  void* workspace = nullptr;
+  int64_t piece = 0;  // tokens per piece
+};
+cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st);
+// Workspace bytes for pieces of `piece` tokens (0: the library's choice), and
+// the tokens per piece that `bytes` have room for (0: not even one tile).
+size_t head_workspace_bytes(int64_t piece, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad, bool nf4);
+int64_t head_piece(size_t bytes, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad, bool nf4);
+
 // ----- per-device launch setup, done once per device and kernel
 
 // Raises the dynamic shared-memory limit of kernel KERN to `bytes` on the

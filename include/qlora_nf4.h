@@ -326,6 +326,74 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
                              const qlora_bf16_t* A, const qlora_bf16_t* B, int r, float scale,
                              qlora_bf16_t* Y, qlora_bf16_t* H_save, void* stream);
 
+/* Head losses: the end of a training step.  A frozen output head W [N, K] (N
+ * = vocabulary, K = hidden width; K % 64 == 0, any N >= 1) turns the hidden
+ * states X [M, K] into logits, a loss per token is taken from them, and the
+ * gradient with respect to X is the dY from which qlora_linear_bwd starts
+ * ("What stays in full precision": gradients flow through the frozen weight,
+ * which gets none).  The logits are never stored.
+ *
+ * The head is given EITHER as W, bf16 [N, K], OR (W NULL) as an NF4 weight in
+ * any codec format: codes, absmax_q, dq_scale, block, dq_block as above
+ * (K % block == 0); an NF4 head is expanded to bf16 once per call, in the
+ * workspace.  With a bf16 head the NF4 arguments are ignored (codes NULL).
+ *
+ * qlora_head_xent, softmax cross entropy with z = X W^T:
+ *     lse[m]  = log sum_j exp z[m, j]
+ *     loss[m] = lse[m] - z[m, labels[m]]
+ *     dX[m]   = dloss[m] (sum_j exp(z[m, j] - lse[m]) W[j] - W[labels[m]])
+ * labels: device int64 [M].  A token whose label is outside [0, N) (such as
+ * the usual -100) is left out: its loss and its row of dX are 0.
+ *
+ * qlora_head_distill, distillation from a teacher's k kept logits with
+ * z = X W^T / T:
+ *     q[m, :] = softmax over the token's kept slots of teacher_logits[m, :] / T
+ *     loss[m] = T^2 sum_s q[m, s] (log q[m, s] - z[m, idx s] + lse[m])
+ *     dX[m]   = dloss[m] T (sum_j exp(z[m, j] - lse[m]) W[j] - sum_s q[m, s] W[idx s])
+ * teacher_idx: device int64 [M, k], the slots' vocabulary entries;
+ * teacher_logits: device [M, k], fp32 (teacher_bf16 = 0) or bf16
+ * (teacher_bf16 = 1); 1 <= k <= QLORA_HEAD_MAX_TARGETS; 1e-4 <= T <= 1e4.  A
+ * slot whose index is outside [0, N) or whose logit is -inf holds nothing (its
+ * logit is not read as a number, so it may be NaN when the index marks it); a
+ * token without slots has loss 0 and a zero row of dX.  An index that appears
+ * twice counts as two slots.
+ *
+ * lse is always log sum exp over the whole vocabulary, of left-out tokens too
+ * (with the temperature applied, for distillation).  loss, lse: device fp32
+ * [M].  dX: device bf16 [M, K], or NULL for the losses alone.  dloss: device
+ * fp32 [M], the gradient of the objective with respect to each loss (a mean
+ * over c tokens: 1 / c), or NULL for ones; without dX it must be NULL.  Where
+ * dloss[m] is 0 the row of dX is 0.  A NaN or an infinity among a token's
+ * logits makes that token's lse, loss and dX NaN; other tokens are untouched.
+ * Logits, statistics and sums are fp32; p - q is rounded to bf16 before the
+ * second product and dX once more at the end.  Outputs must not overlap inputs.
+ *
+ * workspace: qlora_head_workspace bytes, 256-byte aligned.  Tokens are taken
+ * in pieces; with a gradient the workspace holds M' x N bf16 values for a piece
+ * of M' tokens.  piece = 0 asks for the bytes of the library's own choice (at
+ * most 512 MB of such values), another piece for at most that many tokens at
+ * a time; the calls use the largest pieces that fit the workspace they get,
+ * down to 256 tokens (or M, if fewer), below which they return
+ * QLORA_ERR_WORKSPACE.  k = 0 asks for qlora_head_xent, k >= 1 for
+ * qlora_head_distill with k slots; want_dx: dX is not NULL; nf4: an NF4 head.
+ * Results do not depend on other work of the device, and repeat bit for bit
+ * with the same workspace size.
+ * Errors: ARG, SHAPE, UNSUPPORTED, WORKSPACE, CUDA. */
+#define QLORA_HEAD_MAX_TARGETS 256
+int qlora_head_workspace(int64_t M, int64_t N, int64_t K, int k, int want_dx, int nf4, int64_t piece,
+                         size_t* bytes);
+int qlora_head_xent(const qlora_bf16_t* W, const uint8_t* codes, const uint8_t* absmax_q,
+                    const float* dq_scale, int block, int dq_block, int64_t N, int64_t K,
+                    const qlora_bf16_t* X, int64_t M, const int64_t* labels, const float* dloss,
+                    float* loss, float* lse, qlora_bf16_t* dX, void* workspace,
+                    size_t workspace_bytes, void* stream);
+int qlora_head_distill(const qlora_bf16_t* W, const uint8_t* codes, const uint8_t* absmax_q,
+                       const float* dq_scale, int block, int dq_block, int64_t N, int64_t K,
+                       const qlora_bf16_t* X, int64_t M, const int64_t* teacher_idx,
+                       const void* teacher_logits, int teacher_bf16, int k, float temperature,
+                       const float* dloss, float* loss, float* lse, qlora_bf16_t* dX,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads and clears the device status word of the current device (a
  * QLORA_ERR_TIMEOUT left by a bounded wait, else QLORA_OK).  Synchronizes the
  * device. */
