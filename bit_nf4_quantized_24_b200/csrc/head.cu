@@ -48,8 +48,7 @@ constexpr int kNoTarget = 0x7fffffff;
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 
 struct HeadBars {
-  uint64_t full[STAGES];   // this CTA's tiles landed
-  uint64_t peer[STAGES];   // leader: the peer's tiles landed
+  uint64_t full[STAGES];   // leader: both CTAs' tiles landed
   uint64_t empty[STAGES];  // MMAs of the stage completed (multicast by the leader)
   uint64_t acc_full[2];    // accumulator complete (multicast by the leader)
   uint64_t acc_empty[2];   // leader: both CTAs' epilogue warps have read it
@@ -119,8 +118,7 @@ struct HeadEpi {
 // A persistent pair walks its items; two accumulators of 256 TMEM columns let
 // the epilogue of one tile run under the products of the next.
 //   warp 0     TMA producer
-//   warp 1     TMEM allocation; the leader issues the MMAs, the peer reports its
-//              landed stages to the leader
+//   warp 1     TMEM allocation; the leader issues the MMAs
 //   warps 2-5  epilogue, one TMEM lane quarter each: a thread owns a token row
 // Every wait is bounded; on expiry the kernel records kDevTimeout, drains what
 // it issued, frees TMEM and returns.
@@ -134,11 +132,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   HeadBars* bars = reinterpret_cast<HeadBars*>(smem_raw + (base - raw) + OFF_BAR);
   const uint32_t bar0 = base + OFF_BAR;
   auto full = [&](int s) { return bar0 + 8u * s; };
-  auto peer = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
-  auto acc_full = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
-  auto acc_empty = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto acc_full = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto acc_empty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
   const uint32_t dealloc_bar = drain_bar + 8u;
   volatile int* abort = &bars->abort;
 
@@ -170,7 +167,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(peer(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -198,7 +194,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     // --------------------------------------------------------- TMA producer
     if (lane == 0) {
-      const uint32_t bytes = A_BYTES + static_cast<uint32_t>(bnl) * BK * 2;
+      const uint32_t bytes = 2 * (A_BYTES + static_cast<uint32_t>(bnl) * BK * 2);  // of both CTAs
+      const uint32_t full_at_leader = mapa_shared(full(0), 0);
       bool ok = true;
       int n = 0;  // stages issued
       for (int i = first; i < nitems && ok; i += step) {
@@ -208,45 +205,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int k = kbeg; k < kend; ++k) {
           const int s = n % STAGES;
           if (!(ok = wait_bounded(empty(s), ((n / STAGES) & 1) ^ 1, abort, status))) break;
-          mbar_arrive_expect_tx(full(s), bytes);
-          tma_load_2d(base + s * A_BYTES, &tm_a, full(s), k * BK, m0);
-          const uint32_t b_s = base + OFF_B + s * B_BYTES;
+          if (leader) mbar_arrive_expect_tx(full(s), bytes);
+          const uint32_t bar = full_at_leader + 8u * s, b_s = base + OFF_B + s * B_BYTES;
+          tma_load_2d_pair(base + s * A_BYTES, &tm_a, bar, k * BK, m0);
           if (MODE == 0) {
-            tma_load_2d(b_s, &tm_b, full(s), k * BK, n0);
+            tma_load_2d_pair(b_s, &tm_b, bar, k * BK, n0);
           } else {
-            tma_load_2d(b_s, &tm_b, full(s), n0, k * BK);
-            tma_load_2d(b_s + 8192, &tm_b, full(s), n0 + 64, k * BK);
+            tma_load_2d_pair(b_s, &tm_b, bar, n0, k * BK);
+            tma_load_2d_pair(b_s + 8192, &tm_b, bar, n0 + 64, k * BK);
           }
           ++n;
         }
       }
-      if (!ok)  // let the copies already issued land before the CTA exits
-        for (int i = (n > STAGES ? n - STAGES : 0); i < n; ++i) wait_drain(full(i % STAGES), (i / STAGES) & 1);
+      // Let the copies already issued land before the CTA exits.  They report to
+      // the leader, which cannot see the end of a stage that only one CTA has
+      // issued, so each CTA gives its own the time they can need at most.
+      if (!ok && n > 0) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 20000000ull) {
+        }
+      }
     }
   } else if (warp == 1) {
-    // ------------------------------------- MMA issuer (leader), relay (peer)
-    if (lane == 0) {
+    // ----------------------------------------------------------- MMA issuer
+    if (leader && lane == 0) {
       const uint32_t idesc = idesc_bf16(TM, g.bn, false, MODE == 1);
-      const uint32_t peer_at_leader = mapa_shared(peer(0), 0);
       bool ok = true, committed = false;
       int n = 0, t = 0;  // stages and tiles so far
       for (int i = first; i < nitems && ok; i += step, ++t) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
         const uint32_t d = tmem + 256u * (t & 1);
-        if (leader) {
-          if (!(ok = wait_bounded_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
-          tc_fence_after();
-        }
+        if (!(ok = wait_bounded_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
+        tc_fence_after();
         for (int k = kbeg; k < kend; ++k, ++n) {
           const int s = n % STAGES;
           const uint32_t ph = (n / STAGES) & 1;
-          if (!(ok = wait_bounded(full(s), ph, abort, status))) break;
-          if (!leader) {
-            mbar_arrive_remote(peer_at_leader + 8u * s);
-            continue;
-          }
-          if (!(ok = wait_bounded_cluster(peer(s), ph, abort, status))) break;
+          if (!(ok = wait_bounded_cluster(full(s), ph, abort, status))) break;
           tc_fence_after();
           const uint32_t a_s = base + s * A_BYTES, b_s = base + OFF_B + s * B_BYTES;
 #pragma unroll
@@ -258,7 +253,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tc_commit_pair(empty(s));
           committed = true;
         }
-        if (leader && ok) tc_commit_pair(acc_full(t & 1));
+        if (ok) tc_commit_pair(acc_full(t & 1));
       }
       if (!ok && committed) {  // wait for MMAs in flight before TMEM is freed
         tc_commit_pair(drain_bar);
