@@ -11,6 +11,7 @@ Function names follow the C ABI: ``nf4_quantize``, ``nf4_dequantize``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -445,56 +446,72 @@ def head_workspace_bytes(M, N, K, k=0, want_dx=True, nf4=False, piece=0) -> int:
     return b.value
 
 
-def _head_call(fn, what, head, X, k, targets, dloss, outs, workspace, stream):
+@functools.lru_cache(maxsize=256)
+def _head_workspace_cached(device_index, M, N, K, k, want_dx, nf4) -> int:
+    return head_workspace_bytes(M, N, K, k, want_dx, nf4)
+
+
+def _head_call(fn, what, head, X, k, targets, scalars, dloss, outs, workspace, stream):
     """The checks, allocations and call that the two head losses share.
-    targets: the (tensor, dtype, name, shape) checks and the arguments between M
-    and dloss."""
-    if isinstance(head, NF4Weight):
+    targets: (tensor, dtype, name, trailing shape) of what comes between M and
+    dloss, scalars: the numbers that follow them.  A short call is as long as
+    its host work, so nothing is asked or built twice here."""
+    nf4 = isinstance(head, NF4Weight)
+    if nf4:
         N, K = head.N, head.K
-        buffers = [head.codes, head.absmax_q, head.dq_scale]
-        weight = (None, _ptr(head.codes), _ptr(head.absmax_q) if head.absmax_q.numel() else None,
-                  _ptr(head.dq_scale), head.block, head.dq_block)
+        weight = (None, head.codes.data_ptr(), head.absmax_q.data_ptr() if head.absmax_q.numel() else None,
+                  head.dq_scale.data_ptr(), head.block, head.dq_block)
+        tensors = [head.codes, head.absmax_q, head.dq_scale]
     else:
         _req(head, torch.bfloat16, "head")
         if head.dim() != 2:
             raise ValueError(f"head must have shape (N, K), got {tuple(head.shape)}")
         N, K = head.shape
-        buffers = [head]
-        weight = (_ptr(head), None, None, None, BLOCK, DQ_BLOCK)
+        weight = (head.data_ptr(), None, None, None, BLOCK, DQ_BLOCK)
+        tensors = [head]
     if not isinstance(X, torch.Tensor) or X.dim() != 2:
         raise ValueError("X must be a tensor of shape (M, K)")
     M = X.shape[0]
     _req(X, torch.bfloat16, "X", (M, K))
-    checks, args = targets(M)
-    for t, dtype, name, shape in checks:
-        _req(t, dtype, name, shape)
-    if dloss is not None:
-        _req(dloss, torch.float32, "dloss", (M,))
-    dev = X.device
+    args = []
+    for t, dtype, name, tail in targets:
+        _req(t, dtype, name, (M, *tail))
+        args.append(t.data_ptr())
+        tensors.append(t)
     loss, lse, dX = outs if outs is not None else (None, None, None)
-    for t, dtype, name, shape in ((loss, torch.float32, "loss", (M,)), (lse, torch.float32, "lse", (M,)),
-                                  (dX, torch.bfloat16, "dX", (M, K))):
-        if t is not None:
-            _req(t, dtype, name, shape)
     if dX is not None and dloss is None:
         raise ValueError("dX is given but dloss is not")
-    every = buffers + [c[0] for c in checks] + [t for t in (dloss, loss, lse, dX, workspace) if t is not None]
-    if any(t.device != dev for t in every):
-        raise ValueError("all tensors must be on the device of X")
-    if stream is not None and stream.device != dev:
-        raise ValueError("stream must belong to the device of X")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):  # allocations belong to the stream that uses them
-        if loss is None:
-            loss = torch.empty(M, dtype=torch.float32, device=dev)
-        if lse is None:
-            lse = torch.empty(M, dtype=torch.float32, device=dev)
-        if dX is None and dloss is not None:
-            dX = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-        if workspace is None:
-            workspace = torch.empty(head_workspace_bytes(M, N, K, k, dX is not None, isinstance(head, NF4Weight)),
-                                    dtype=torch.uint8, device=dev)
-        _check(fn(*weight, N, K, _ptr(X), M, *args, _ptr(dloss), _ptr(loss), _ptr(lse), _ptr(dX), _ptr(workspace),
-                  workspace.numel() * workspace.element_size(), _stream()), what)
+    for t, dtype, name, shape in ((dloss, torch.float32, "dloss", (M,)), (loss, torch.float32, "loss", (M,)),
+                                  (lse, torch.float32, "lse", (M,)), (dX, torch.bfloat16, "dX", (M, K))):
+        if t is not None:
+            _req(t, dtype, name, shape)
+            tensors.append(t)
+    if workspace is not None:
+        tensors.append(workspace)
+    dev = X.device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError("all tensors must be on the device of X")
+    if stream is not None or dev.index != torch.cuda.current_device():
+        if stream is not None and stream.device != dev:
+            raise ValueError("stream must belong to the device of X")
+        # what is allocated belongs to the stream that uses it
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return _head_call(fn, what, head, X, k, targets, scalars, dloss, outs, workspace, None)
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty(M, dtype=torch.float32, device=dev)
+    if dX is None and dloss is not None:
+        dX = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        nbytes = _head_workspace_cached(dev.index, M, N, K, k, dX is not None, nf4)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(fn(*weight, N, K, X.data_ptr(), M, *args, *scalars, None if dloss is None else dloss.data_ptr(),
+              loss.data_ptr(), lse.data_ptr(), None if dX is None else dX.data_ptr(), workspace.data_ptr(), nbytes,
+              torch._C._cuda_getCurrentRawStream(dev.index)), what)
     return loss, lse, dX
 
 
@@ -506,10 +523,8 @@ def qlora_head_xent(head, X: torch.Tensor, labels: torch.Tensor, dloss: torch.Te
     [M] each, and with dloss (fp32 [M], the objective's gradient with respect to
     each loss) dX = dloss (softmax(Z) - onehot(labels)) head in bf16, else None.
     outs: (loss, lse, dX) tensors to write, any of them None."""
-    def targets(M):
-        return [(labels, torch.int64, "labels", (M,))], (_ptr(labels),)
-
-    return _head_call(lib().qlora_head_xent, "qlora_head_xent", head, X, 0, targets, dloss, outs, workspace, stream)
+    return _head_call(lib().qlora_head_xent, "qlora_head_xent", head, X, 0, ((labels, torch.int64, "labels", ()),), (),
+                      dloss, outs, workspace, stream)
 
 
 def qlora_head_distill(head, X: torch.Tensor, teacher_idx: torch.Tensor, teacher_logits: torch.Tensor,
@@ -526,14 +541,11 @@ def qlora_head_distill(head, X: torch.Tensor, teacher_idx: torch.Tensor, teacher
     if not isinstance(teacher_logits, torch.Tensor) or teacher_logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("teacher_logits must be a torch.float32 or torch.bfloat16 tensor")
 
-    def targets(M):
-        return ([(teacher_idx, torch.int64, "teacher_idx", (M, k)),
-                 (teacher_logits, teacher_logits.dtype, "teacher_logits", (M, k))],
-                (_ptr(teacher_idx), _ptr(teacher_logits), int(teacher_logits.dtype == torch.bfloat16), k,
-                 float(temperature)))
-
-    return _head_call(lib().qlora_head_distill, "qlora_head_distill", head, X, k, targets, dloss, outs, workspace,
-                      stream)
+    targets = ((teacher_idx, torch.int64, "teacher_idx", (k,)),
+               (teacher_logits, teacher_logits.dtype, "teacher_logits", (k,)))
+    scalars = (int(teacher_logits.dtype == torch.bfloat16), k, float(temperature))
+    return _head_call(lib().qlora_head_distill, "qlora_head_distill", head, X, k, targets, scalars, dloss, outs,
+                      workspace, stream)
 
 
 def gemm_resident_pairs(mode: int = 0) -> int:

@@ -66,6 +66,7 @@ struct HeadGrid {
   int nwhole, ntail, nsplit;
   int band;                   // token tiles walked together
   int bn;                     // outputs per tile (a multiple of 32; 256 for MODE 1)
+  int abox;                   // token rows of the A box: UM, or fewer when the whole piece fits one CTA
 };
 
 __device__ __forceinline__ void tile_of(const HeadGrid& g, int L, int& mt, int& nt) {
@@ -126,6 +127,7 @@ template <int MODE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_head(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int numK, HeadGrid g,
            HeadEpi p, int* status) {
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -182,10 +184,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
   }
+  if (g.abox < UM) {  // the rows that no copy writes hold zeros
+    for (int i = threadIdx.x; i < STAGES * A_BYTES / 16; i += NUM_THREADS) st_shared_v4(base + 16 * i, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   if (warp == 1) {
     tmem_alloc_pair(bar0 + static_cast<uint32_t>(offsetof(HeadBars, tmem_base)), TMEM_COLS);
     tmem_relinquish_pair();
   }
+  pdl_wait();  // everything above is local to the pair
   tc_fence_before();
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
@@ -194,7 +201,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     // --------------------------------------------------------- TMA producer
     if (lane == 0) {
-      const uint32_t bytes = 2 * (A_BYTES + static_cast<uint32_t>(bnl) * BK * 2);  // of both CTAs
+      const bool one = g.abox < UM;  // all tokens in the leader's rows, of which abox are loaded
+      const uint32_t bytes = ((one ? 1 : 2) * g.abox + 2 * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
       const uint32_t full_at_leader = mapa_shared(full(0), 0);
       bool ok = true;
       int n = 0;  // stages issued
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!(ok = wait_bounded(empty(s), ((n / STAGES) & 1) ^ 1, abort, status))) break;
           if (leader) mbar_arrive_expect_tx(full(s), bytes);
           const uint32_t bar = full_at_leader + 8u * s, b_s = base + OFF_B + s * B_BYTES;
-          tma_load_2d_pair(base + s * A_BYTES, &tm_a, bar, k * BK, m0);
+          if (!one || leader) tma_load_2d_pair(base + s * A_BYTES, &tm_a, bar, k * BK, m0);
           if (MODE == 0) {
             tma_load_2d_pair(b_s, &tm_b, bar, k * BK, n0);
           } else {
@@ -328,6 +336,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int j = 0; j < d; ++j) e[j] += e[j + d];
           sum += e[0];
         }
+        if (p.e && live && nt == g.ntiles - 1)  // the pitch may reach past the last tile
+          for (int64_t col = n0 + g.bn; col < p.lde; col += 8)
+            *reinterpret_cast<uint4*>(erow + (col - n0)) = make_uint4(0u, 0u, 0u, 0u);
         if (live)
           p.part[static_cast<int64_t>(nt) * p.rows + row] =
               make_float2(mx == -INFINITY ? mx : ref, sum);
@@ -420,6 +431,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Sum of the pieces of the split gradient tiles in piece order, times the row's
 // factor, rounded once to bf16.  Thread: 8 consecutive outputs of a row.
 __global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ split, HeadGrid g, HeadEpi p) {
+  pdl_trigger();
+  pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   constexpr int per_tile = TM * (TN / 8);
   const int t = static_cast<int>(i / per_tile), w = static_cast<int>(i % per_tile);
@@ -455,6 +468,8 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
                                                       int k, int N, float inv_t, int bn, int ntiles,
                                                       int* __restrict__ sidx, float* __restrict__ logq,
                                                       uint16_t* __restrict__ off) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ int key[256], sorted[256];
   __shared__ float val[256];
   const int64_t row = blockIdx.x;
@@ -507,6 +522,8 @@ __global__ void __launch_bounds__(1024)
                  const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float* __restrict__ ztgt,
                  float temp, const float* __restrict__ dloss, float* __restrict__ loss, float* __restrict__ lse,
                  float2* __restrict__ lse2, float* __restrict__ rscale) {
+  pdl_trigger();
+  pdl_wait();
   __shared__ float2 sh[32][33];
   const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
   const int row0 = blockIdx.x * 32;
@@ -561,22 +578,28 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
   return bf16x2_bits(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
 }
 
-// e -> p - q in place, one block per row: p = e exp2(reference - lse), rounded
-// to bf16 again; target columns hold exp(z - lse) - q from their fp32 logits
-// (cross entropy: expm1, exact where p is near 1).
+// e -> p - q in place: p = e exp2(reference - lse), rounded to bf16 again;
+// target columns hold exp(z - lse) - q from their fp32 logits (cross entropy:
+// expm1, exact where p is near 1).  Block (x, y): row x, the y-th share of its
+// columns (several blocks per row where rows are few, to fill the GPU).
 __global__ void __launch_bounds__(256)
-    k_head_scale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int bn, int rows, int N,
+    k_head_scale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int bn, int ntiles, int rows,
                  const float2* __restrict__ lse2, const float* __restrict__ rscale, const int64_t* __restrict__ labels,
                  const int* __restrict__ sidx, const float* __restrict__ logq, int k,
                  const float* __restrict__ ztgt) {
+  pdl_trigger();
+  pdl_wait();
   const int row = blockIdx.x;
   if (rscale[row] == 0.0f) return;  // its gradient is written as zeros
   const float2 l2 = lse2[row];  // subtracted in two steps: their sum would round off digits of z - lse
   uint16_t* er = e + static_cast<int64_t>(row) * lde;
   uint4* v = reinterpret_cast<uint4*>(er);
   const int chunks = static_cast<int>(lde / 8), per_tile = bn / 8;
-  for (int c = threadIdx.x; c < chunks; c += 256) {
-    const float f = exp2f(part[static_cast<int64_t>(c / per_tile) * rows + row].x - l2.x - l2.y);
+  const int share = (chunks + gridDim.y - 1) / gridDim.y;
+  const int c0 = blockIdx.y * share, c1 = min(chunks, c0 + share);
+  for (int c = c0 + threadIdx.x; c < c1; c += 256) {
+    const int t = min(c / per_tile, ntiles - 1);
+    const float f = exp2f(part[static_cast<int64_t>(t) * rows + row].x - l2.x - l2.y);
     uint4 x = v[c];
     x.x = scale_pair(x.x, f);
     x.y = scale_pair(x.y, f);
@@ -585,16 +608,18 @@ __global__ void __launch_bounds__(256)
     v[c] = x;
   }
   __syncthreads();
+  const int64_t y0 = 8ll * c0, y1 = 8ll * c1;
   if (labels) {
-    if (threadIdx.x == 0) {
+    const int64_t y = labels[row];
+    if (threadIdx.x == 0 && y >= y0 && y < y1) {
       const float d = expm1f((ztgt[row] - l2.x - l2.y) * kLn2);
-      er[labels[row]] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
+      er[y] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
     }
   } else {
     const int64_t at = static_cast<int64_t>(row) * k;
     for (int j = threadIdx.x; j < k; j += 256) {
       const int y = sidx[at + j];
-      if (y == kNoTarget || (j > 0 && sidx[at + j - 1] == y)) continue;
+      if (y < y0 || y >= y1 || (j > 0 && sidx[at + j - 1] == y)) continue;  // kNoTarget is past every share
       float d = exp2f(ztgt[at + j] - l2.x - l2.y);
       for (int o = j; o < k && sidx[at + o] == y; ++o) d -= expf(logq[at + o]);
       er[y] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
@@ -614,8 +639,10 @@ cudaLaunchConfig_t pair_config(int pairs, cudaStream_t st, cudaLaunchAttribute* 
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -630,7 +657,7 @@ int head_pairs() {
   }
   int v = cache[d].load(std::memory_order_relaxed);
   if (v == 0) {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     int a = 0, b = 0;
     const cudaLaunchConfig_t cfg = pair_config(1, nullptr, attr);
     if (smem_limit_once<k_head<0>>(SMEM_ALLOC) == cudaSuccess &&
@@ -653,15 +680,40 @@ int band_of(int64_t mtiles, int64_t contraction) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(mtiles, (48ll << 20) / (TM * contraction * 2))));
 }
 
-// Tiles of the logits product.
+// Rows of the A box.  A box reaching past the last token is filled with zeros
+// at a cost: with one token and a full box the logits product of a 32000 x 4096
+// head took 85 us, with 64 tokens 56 us.
+int a_box(int64_t rows) { return rows < UM ? static_cast<int>((rows + 7) / 8 * 8) : UM; }
+
+// Tiles of the logits product.  Their width is the one whose rounds over the
+// resident pairs cost least, 256 if nothing is clearly better.  A stage of a
+// tile costs the bytes a CTA brings from L2 for it (128 token rows and bn / 2 of
+// the head): a pair's MMA of width 256 takes 512 cycles per stage, and its 32 KB
+// per CTA are 64 B per cycle, about what L2 delivers, so narrower tiles only pay
+// where they save a round.  With a single token tile the head's rows alone count
+// (they come from HBM): 32000 entries are two rounds of 256 on 74 pairs, or two
+// of 224.
 HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
   HeadGrid g{};
   g.mtiles = static_cast<int>((rows + TM - 1) / TM);
   g.bn = TN;
+  const int P = head_pairs();
+  if (P > 0) {
+    double best = 0.0;
+    for (int bn = TN; bn >= 128; bn -= 32) {
+      const int64_t rounds = (g.mtiles * ((N + bn - 1) / bn) + P - 1) / P;
+      const double cost = static_cast<double>(rounds) * (g.mtiles == 1 ? bn : UM + bn / 2);
+      if (bn == TN || cost < 0.97 * best) {
+        best = cost;
+        g.bn = bn;
+      }
+    }
+  }
   g.ntiles = static_cast<int>((N + g.bn - 1) / g.bn);
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
   g.band = band_of(g.mtiles, K);
+  g.abox = a_box(rows);
   return g;
 }
 
@@ -675,6 +727,7 @@ HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
   g.band = g.mtiles;
+  g.abox = a_box(rows);
   const int64_t numK = (N + BK - 1) / BK;
   const int P = head_pairs();
   if (P <= 0) return g;
@@ -759,7 +812,7 @@ cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, int64_t cont
   const int64_t items = int64_t(g.nwhole) + int64_t(g.ntail) * g.nsplit;
   int P = head_pairs();
   if (P <= 0) P = std::max(1, device_sm_count() / 2);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = pair_config(static_cast<int>(std::min<int64_t>(items, P)), st, attr);
   return cudaLaunchKernelEx(&cfg, k_head<MODE>, a, b, static_cast<int>((contraction + BK - 1) / BK), g, p,
                             device_status_ptr());
@@ -800,7 +853,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     const HeadGrid g = logits_grid(rows, a.N, a.K);
     const uint16_t* X = a.X + r0 * a.K;
     CUtensorMap ma, mb;
-    if (!make_map(&ma, BF16, X, a.K, rows, a.K * 2, BK, UM, SW) ||
+    if (!make_map(&ma, BF16, X, a.K, rows, a.K * 2, BK, g.abox, SW) ||
         !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, BK, g.bn / 2, SW))
       return cudaErrorInvalidValue;
     HeadEpi p{};
@@ -820,18 +873,18 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
       const int64_t* idx = a.teacher_idx + r0 * a.k;
       const float inv_t = 1.0f / a.temperature;
       if (a.teacher_bf16)
-        err = launch_ex(k_head_targets<__nv_bfloat16>, grid, block, 0, st, false, idx,
+        err = launch_ex(k_head_targets<__nv_bfloat16>, grid, block, 0, st, true, idx,
                         static_cast<const __nv_bfloat16*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.bn,
                         g.ntiles, s.sidx, s.logq, s.off);
       else
-        err = launch_ex(k_head_targets<float>, grid, block, 0, st, false, idx,
+        err = launch_ex(k_head_targets<float>, grid, block, 0, st, true, idx,
                         static_cast<const float*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.bn, g.ntiles,
                         s.sidx, s.logq, s.off);
       if (err != cudaSuccess) return err;
     }
     err = launch_head<0>(ma, mb, a.K, g, p, st);
     if (err != cudaSuccess) return err;
-    err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(1024), 0, st, false,
+    err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(1024), 0, st, true,
                     static_cast<const float2*>(s.part), g.ntiles, p.rows, p.cols, p.labels,
                     static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
                     static_cast<const float*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
@@ -840,13 +893,17 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
       if (err != cudaSuccess) return err;
       continue;
     }
-    err = launch_ex(k_head_scale, dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, false, s.e, lde,
-                    static_cast<const float2*>(s.part), g.bn, p.rows, p.cols, static_cast<const float2*>(s.lse2),
+    // At least 2048 elements per block, and as many blocks per row as give about eight to each SM.
+    const int64_t shares =
+        std::max<int64_t>(1, std::min<int64_t>(lde / 2048, (8ll * device_sm_count() + rows - 1) / rows));
+    err = launch_ex(k_head_scale, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(shares)), dim3(256), 0, st,
+                    true, s.e, lde, static_cast<const float2*>(s.part), g.bn, g.ntiles, p.rows,
+                    static_cast<const float2*>(s.lse2),
                     static_cast<const float*>(s.rscale), p.labels, static_cast<const int*>(s.sidx),
                     static_cast<const float*>(s.logq), a.k, static_cast<const float*>(s.ztgt));
     if (err != cudaSuccess) return err;
     const HeadGrid d = grad_grid(rows, a.N, a.K);
-    if (!make_map(&ma, BF16, s.e, lde, rows, lde * 2, BK, UM, SW) ||
+    if (!make_map(&ma, BF16, s.e, lde, rows, lde * 2, BK, d.abox, SW) ||
         !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, 64, BK, SW))
       return cudaErrorInvalidValue;
     HeadEpi q{};
@@ -858,7 +915,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     err = launch_head<1>(ma, mb, a.N, d, q, st);
     if (err == cudaSuccess && d.ntail)
       err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (TN / 8) / 256))), dim3(256), 0, st,
-                      false, static_cast<const float*>(s.split), d, q);
+                      true, static_cast<const float*>(s.split), d, q);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

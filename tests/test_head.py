@@ -265,13 +265,13 @@ def test_confident_tokens_keep_the_digits_of_their_gradient(L):
 @gpu
 @pytest.mark.parametrize("piece", [256, 512])
 def test_pieces_of_tokens(L, piece):
-    """A smaller workspace takes fewer tokens at a time: the losses are the same bits, the gradient the same within
-    its rounding (other tiles are split), and the rows behind the last piece are written once."""
+    """A smaller workspace takes fewer tokens at a time: the same results within their rounding (tile widths and split
+    tiles follow the piece's size), the same bits when repeated, and the rows behind the last piece written once."""
     M, N, K = 900, 3001, 512
     head, values, X, labels, g = make(21, M, N, K)
     dloss = torch.rand(M, generator=g).cuda()
     ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)
-    whole = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    compare(qb.qlora_head_xent(head, X, labels, dloss=dloss), ref)
     nbytes = qb.head_workspace_bytes(M, N, K, piece=piece)
     assert nbytes < qb.head_workspace_bytes(M, N, K)
     ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
@@ -280,7 +280,6 @@ def test_pieces_of_tokens(L, piece):
     got = qb.qlora_head_xent(head, X, labels, dloss=dloss, outs=outs, workspace=ws)
     assert all(a is b for a, b in zip(got, outs))
     compare(got, ref)
-    assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
     again = qb.qlora_head_xent(head, X, labels, dloss=dloss, workspace=ws)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
     idx, t = teacher(g, M, N, 9, False)
