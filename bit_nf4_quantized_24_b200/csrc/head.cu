@@ -9,20 +9,28 @@
 // the teacher's kept logits over T for distillation.
 //
 // The logits never reach memory.  A product kernel (k_head<0>) leaves, for each
-// row and each tile of the vocabulary, the tile's maximum and its sum of
-// exponentials, and the target logits it meets, all in fp32 straight from the
-// accumulator; k_head_stats joins them into lse and loss.  For the gradient the
-// same kernel also writes e = exp(z - tile maximum) in bf16 for a piece of the
-// tokens; once lse is known, k_head_scale turns e into p - q in place (one
-// multiplication by exp(tile maximum - lse); the target columns are computed
-// from their fp32 logits, because p - 1 from a rounded p would be noise for a
-// confident token), and k_head<1> multiplies by W again.  So a loss with its
-// gradient costs two products; computing p from the logits a second time would
-// need three, and keeping the logits themselves in bf16 would cost accuracy:
-// a rounding error of 2^-9 of a logit near 20 is 4 % of its p, while the same
-// rounding of e is 2^-9 of p.
+// row and each column segment of its tiles, a reference near the segment's
+// maximum and the sum of exponentials relative to it, and the target logits it
+// meets, all in fp32 straight from the accumulator; k_head_stats joins them into
+// lse and loss.  For the gradient the same kernel also writes e = exp(z) in bf16
+// for a piece of the tokens, and k_head<1> multiplies e by W once lse is known:
+// p = e exp(-lse) is a factor of the whole row, so it waits for the epilogue,
+// and only the target columns of e change in between (they hold p - q, computed
+// from their fp32 logits: p - 1 from a rounded p would be noise for a confident
+// token).  So a loss with its gradient costs two products and no pass over the
+// exponentials.
+//  - Computing p from the logits a second time would need three products.
+//  - Keeping the logits themselves in bf16 would cost accuracy: a rounding error
+//    of 2^-9 of a logit near 20 is 4 % of its p; the same rounding of e is 2^-9 of
+//    p.
+//  - e needs no maximum subtracted as long as it fits the exponent of bf16, which
+//    is that of fp32: a segment whose maximum is within 2^-64 .. 2^64 is stored as
+//    it is.  A segment outside (a logit past 44) is stored relative to its own
+//    reference, and k_head_rescale then brings the rows that have one to a common
+//    reference, by exact powers of two.
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 
 #include "internal.h"
 
@@ -32,24 +40,25 @@ namespace {
 
 constexpr int UM = 128;      // token rows of each CTA of a pair
 constexpr int TM = 2 * UM;   // token rows of a tile
-constexpr int TN = 256;      // largest tile width (vocabulary entries or outputs)
+constexpr int TN = 256;      // largest width of one accumulator (vocabulary entries or outputs)
 constexpr int BK = 64;       // contraction per stage
-constexpr int STAGES = 6;
 constexpr int A_BYTES = UM * BK * 2;
-constexpr int B_BYTES = TN / 2 * BK * 2;
-constexpr int OFF_B = STAGES * A_BYTES;
-constexpr int OFF_BAR = OFF_B + STAGES * B_BYTES;
+constexpr int B_BYTES = TN / 2 * BK * 2;  // per accumulator
+constexpr int RING_BYTES = 192 * 1024;    // 6 stages of 32 KB (NH = 1) or 4 of 48 KB (NH = 2)
+constexpr int MAX_STAGES = 6;
+constexpr int OFF_BAR = RING_BYTES;
 constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignment
-constexpr int EPI_WARPS = 4;
+constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int kNoTarget = 0x7fffffff;
+constexpr float kFits = 64.0f;  // |reference| (log2) up to which e is stored without it
 
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 
 struct HeadBars {
-  uint64_t full[STAGES];   // leader: both CTAs' tiles landed
-  uint64_t empty[STAGES];  // MMAs of the stage completed (multicast by the leader)
+  uint64_t full[MAX_STAGES];   // leader: both CTAs' tiles landed
+  uint64_t empty[MAX_STAGES];  // MMAs of the stage completed (multicast by the leader)
   uint64_t acc_full[2];    // accumulator complete (multicast by the leader)
   uint64_t acc_empty[2];   // leader: both CTAs' epilogue warps have read it
   uint64_t drain;          // leader: used only when aborting
@@ -62,10 +71,13 @@ static_assert(sizeof(HeadBars) <= 256, "barrier block");
 // Work items: whole tiles, then nsplit pieces (of the contraction) of each of
 // the last ntail tiles, as in the fused NF4 GEMM.
 struct HeadGrid {
-  int mtiles, ntiles;         // token tiles of 256, output tiles of bn
+  int mtiles, ntiles;         // token tiles of 256, output tiles of tn
   int nwhole, ntail, nsplit;
   int band;                   // token tiles walked together
-  int bn;                     // outputs per tile (a multiple of 32; 256 for MODE 1)
+  int nh;                     // accumulators per tile, side by side along the outputs
+  int bn;                     // outputs per accumulator (a multiple of 32; 256 if nh = 2 or MODE 1)
+  int tn;                     // outputs per tile, nh bn
+  int sw;                     // outputs of the first of a tile's two column segments (one per epilogue group)
   int abox;                   // token rows of the A box: UM, or fewer when the whole piece fits one CTA
 };
 
@@ -97,36 +109,43 @@ struct HeadEpi {
   int cols;         // MODE 0: N; MODE 1: K
   // MODE 0
   float c;                   // log2(e) / T
-  float2* part;              // [ntiles][rows]: (maximum * c, sum of exp2(z c - maximum c))
+  float2* part;              // [2 ntiles][rows], per column segment: (reference n, sum of exp2(z c - n))
   uint16_t* e;               // [rows][lde] (nullable)
   int64_t lde;
   const int64_t* labels;     // [rows] (cross entropy), or
   const int* sidx;           // [rows][k] targets in ascending order, and
-  const uint16_t* off;       // [rows][ntiles + 1] first target of each tile
+  const uint16_t* off;       // [rows][2 ntiles + 1] first target of each column segment
   int k;
-  float* ztgt;               // [rows][k] target logits (times c)
+  float2* ztgt;              // [rows][k] target logits: (z c - n, n)
   // MODE 1
-  const float* rscale;       // [rows] factor of the row (0: the row is written as zeros)
+  const float2* rscale;      // [rows] factors (x, y) of the row (y = 0: the row is written as zeros)
   uint16_t* out;             // [rows][cols]
   float* split;              // fp32 sums of the split tiles' pieces
 };
 
-// D = A B^T by pairs of CTAs (cta_group::2): 256 tokens x up to 256 outputs per
-// tile, each CTA holding 128 token rows and half of the output rows of each
-// stage, both brought by TMA.  MODE 0: A = X, B = W (K-major).  MODE 1: A = p - q
-// [rows, N], B = W with its rows as the contraction (MN-major).
+// D = A B^T by pairs of CTAs (cta_group::2): 256 tokens x NH accumulators of up
+// to 256 outputs per tile, each CTA holding 128 token rows and half of the
+// output rows of each stage, both brought by TMA.  MODE 0: A = X, B = W
+// (K-major).  MODE 1: A = p - q [rows, N], B = W with its rows as the
+// contraction (MN-major).
 //
-// A persistent pair walks its items; two accumulators of 256 TMEM columns let
-// the epilogue of one tile run under the products of the next.
+// A persistent pair walks its items.  NH = 1: two accumulators alternate, so the
+// epilogue of one tile runs under the products of the next.  NH = 2: the two
+// accumulators make one tile of 512 outputs, which brings a quarter fewer bytes
+// from L2 per product.
 //   warp 0     TMA producer
 //   warp 1     TMEM allocation; the leader issues the MMAs
-//   warps 2-5  epilogue, one TMEM lane quarter each: a thread owns a token row
+//   warps 2-9  epilogue in two groups of four, one column segment each, a warp
+//              one TMEM lane quarter: a thread owns a token row
 // Every wait is bounded; on expiry the kernel records kDevTimeout, drains what
 // it issued, frees TMEM and returns.
-template <int MODE>
+template <int MODE, int NH>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_head(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int numK, HeadGrid g,
            HeadEpi p, int* status) {
+  constexpr int STAGE_BYTES = A_BYTES + NH * B_BYTES;
+  constexpr int STAGES = RING_BYTES / STAGE_BYTES;
+  static_assert(STAGES <= MAX_STAGES, "barrier block");
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -134,10 +153,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   HeadBars* bars = reinterpret_cast<HeadBars*>(smem_raw + (base - raw) + OFF_BAR);
   const uint32_t bar0 = base + OFF_BAR;
   auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto acc_full = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  auto acc_empty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  auto empty = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
+  auto acc_full = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + a); };
+  auto acc_empty = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 4);
   const uint32_t dealloc_bar = drain_bar + 8u;
   volatile int* abort = &bars->abort;
 
@@ -173,7 +192,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full(a), 1);
-      mbar_init(acc_empty(a), 2 * EPI_WARPS);
+      // NH = 1: both groups read each accumulator; NH = 2: one group each
+      mbar_init(acc_empty(a), 2 * EPI_WARPS / NH);
     }
     mbar_init(drain_bar, 1);
     mbar_init(dealloc_bar, 1);
@@ -185,7 +205,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&tm_b);
   }
   if (g.abox < UM) {  // the rows that no copy writes hold zeros
-    for (int i = threadIdx.x; i < STAGES * A_BYTES / 16; i += NUM_THREADS) st_shared_v4(base + 16 * i, 0u, 0u, 0u, 0u);
+    for (int s = 0; s < STAGES; ++s)
+      for (int i = threadIdx.x; i < A_BYTES / 16; i += NUM_THREADS)
+        st_shared_v4(base + s * STAGE_BYTES + 16 * i, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
   if (warp == 1) {
@@ -202,25 +224,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // --------------------------------------------------------- TMA producer
     if (lane == 0) {
       const bool one = g.abox < UM;  // all tokens in the leader's rows, of which abox are loaded
-      const uint32_t bytes = ((one ? 1 : 2) * g.abox + 2 * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
+      const uint32_t bytes = ((one ? 1 : 2) * g.abox + 2 * NH * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
       const uint32_t full_at_leader = mapa_shared(full(0), 0);
       bool ok = true;
       int n = 0;  // stages issued
       for (int i = first; i < nitems && ok; i += step) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
-        const int m0 = mt * TM + static_cast<int>(rank) * UM, n0 = nt * g.bn + static_cast<int>(rank) * bnl;
+        const int m0 = mt * TM + static_cast<int>(rank) * UM, n0 = nt * g.tn + static_cast<int>(rank) * bnl;
         for (int k = kbeg; k < kend; ++k) {
           const int s = n % STAGES;
           if (!(ok = wait_bounded(empty(s), ((n / STAGES) & 1) ^ 1, abort, status))) break;
           if (leader) mbar_arrive_expect_tx(full(s), bytes);
-          const uint32_t bar = full_at_leader + 8u * s, b_s = base + OFF_B + s * B_BYTES;
-          if (!one || leader) tma_load_2d_pair(base + s * A_BYTES, &tm_a, bar, k * BK, m0);
-          if (MODE == 0) {
-            tma_load_2d_pair(b_s, &tm_b, bar, k * BK, n0);
-          } else {
-            tma_load_2d_pair(b_s, &tm_b, bar, n0, k * BK);
-            tma_load_2d_pair(b_s + 8192, &tm_b, bar, n0 + 64, k * BK);
+          const uint32_t bar = full_at_leader + 8u * s, a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
+          if (!one || leader) tma_load_2d_pair(a_s, &tm_a, bar, k * BK, m0);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            if (MODE == 0) {
+              tma_load_2d_pair(b_s + h * B_BYTES, &tm_b, bar, k * BK, n0 + h * TN);
+            } else {
+              tma_load_2d_pair(b_s + h * B_BYTES, &tm_b, bar, n0 + h * TN, k * BK);
+              tma_load_2d_pair(b_s + h * B_BYTES + 8192, &tm_b, bar, n0 + h * TN + 64, k * BK);
+            }
           }
           ++n;
         }
@@ -243,25 +268,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int i = first; i < nitems && ok; i += step, ++t) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
-        const uint32_t d = tmem + 256u * (t & 1);
-        if (!(ok = wait_bounded_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
+        if (NH == 1) {
+          ok = wait_bounded_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status);
+        } else {
+          ok = wait_bounded_cluster(acc_empty(0), (t & 1) ^ 1, abort, status) &&
+               wait_bounded_cluster(acc_empty(1), (t & 1) ^ 1, abort, status);
+        }
+        if (!ok) break;
         tc_fence_after();
+        const uint32_t d = NH == 1 ? tmem + 256u * (t & 1) : tmem;
         for (int k = kbeg; k < kend; ++k, ++n) {
           const int s = n % STAGES;
           const uint32_t ph = (n / STAGES) & 1;
           if (!(ok = wait_bounded_cluster(full(s), ph, abort, status))) break;
           tc_fence_after();
-          const uint32_t a_s = base + s * A_BYTES, b_s = base + OFF_B + s * B_BYTES;
+          const uint32_t a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t bd =
-                MODE == 0 ? desc_sw128(b_s + kk * 32, 16, 1024) : desc_sw128(b_s + kk * 2048, 8192, 1024);
-            tc_mma_f16_pair(d, desc_sw128(a_s + kk * 32, 16, 1024), bd, idesc, (k > kbeg || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              const uint32_t b_h = b_s + h * B_BYTES;
+              const uint64_t bd =
+                  MODE == 0 ? desc_sw128(b_h + kk * 32, 16, 1024) : desc_sw128(b_h + kk * 2048, 8192, 1024);
+              tc_mma_f16_pair(d + 256u * h, desc_sw128(a_s + kk * 32, 16, 1024), bd, idesc,
+                              (k > kbeg || kk > 0) ? 1u : 0u);
+            }
           }
           tc_commit_pair(empty(s));
           committed = true;
         }
-        if (ok) tc_commit_pair(acc_full(t & 1));
+        if (ok) {
+          if (NH == 1) {
+            tc_commit_pair(acc_full(t & 1));
+          } else {
+            tc_commit_pair(acc_full(0));
+            tc_commit_pair(acc_full(1));
+          }
+        }
       }
       if (!ok && committed) {  // wait for MMAs in flight before TMEM is freed
         tc_commit_pair(drain_bar);
@@ -270,23 +313,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    const int quad = warp & 3;  // TMEM lanes 32 quad .. 32 quad + 31
+    const int quad = warp & 3;         // TMEM lanes 32 quad .. 32 quad + 31
+    const int h = (warp - 2) >> 2;     // column segment
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t empty_at_leader = mapa_shared(acc_empty(0), 0);
+    const int cseg = h * g.sw;                         // the segment's first column in the tile
+    const int cwidth = h == 0 ? g.sw : g.tn - g.sw;    // and its width
     int t = 0;
     for (int i = first; i < nitems; i += step, ++t) {
       int mt, nt, kbeg, kend, tail, z;
       item(i, mt, nt, kbeg, kend, tail, z);
       const int row0 = mt * TM + static_cast<int>(rank) * UM + quad * 32;  // the warp's first row
       const int row = row0 + lane;
-      const int n0 = nt * g.bn;
-      const bool landed = wait_bounded(acc_full(t & 1), (t >> 1) & 1, abort, status);
+      const int n0 = nt * g.tn + cseg;  // the segment's first output
+      const int a = NH == 1 ? (t & 1) : h;
+      const bool landed = wait_bounded(acc_full(a), NH == 1 ? (t >> 1) & 1 : t & 1, abort, status);
       if (!__all_sync(0xffffffffu, landed)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + lane_base + 256u * (t & 1);
+      const uint32_t acc = tmem + lane_base + (NH == 1 ? 256u * a + cseg : 256u * h);
       if (MODE == 0 && row0 < p.rows) {
         const bool live = row < p.rows;
-        const int ncols = min(g.bn, p.cols - n0);
+        const int ncols = max(0, min(cwidth, p.cols - n0));
         float mx = -INFINITY;
 #pragma unroll 1
         for (int col = 0; col < ncols; col += 32) {
@@ -302,13 +349,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (col + j < ncols) mx = fmaxf(mx, __uint_as_float(v[j]));
           }
         }
-        // The tile's reference in units of log2: kept as rounded here, so that
-        // sum * exp2(reference) does not depend on that rounding.
-        // (A tile whose logits are all -inf or NaN is summed around 0.)
-        const float ref = mx == -INFINITY ? 0.0f : __fmul_rn(mx, p.c);
+        // The segment's reference in units of log2 is a whole number, so taking it
+        // off and putting it back are exact.  (A segment whose logits are all -inf
+        // or NaN is summed around 0.)
+        const float ref = mx == -INFINITY ? 0.0f : rintf(mx * p.c);
+        const float back = exp2f(fabsf(ref) <= kFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
+        const __nv_bfloat162 back2 = __float2bfloat162_rn(back);
         float sum = 0.0f;
         uint16_t* erow = p.e ? p.e + static_cast<int64_t>(row) * p.lde + n0 : nullptr;
-        const int ewidth = static_cast<int>(min(static_cast<int64_t>(g.bn), p.lde - n0));
+        const int ewidth = static_cast<int>(min(static_cast<int64_t>(cwidth), p.lde - n0));
 #pragma unroll 1
         for (int col = 0; col < ewidth; col += 32) {
           uint32_t v[32];
@@ -321,29 +370,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (col + 32 > ncols && col + j >= ncols) e[j] = 0.0f;
           }
           if (p.e && live) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 x = __hmul2(__floats2bfloat162_rn(e[2 * j], e[2 * j + 1]), back2);
+              w[j] = *reinterpret_cast<const uint32_t*>(&x);
+            }
             uint4* dst = reinterpret_cast<uint4*>(erow + col);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[q] = make_uint4(bf16x2_bits(e[8 * q], e[8 * q + 1]), bf16x2_bits(e[8 * q + 2], e[8 * q + 3]),
-                                  bf16x2_bits(e[8 * q + 4], e[8 * q + 5]), bf16x2_bits(e[8 * q + 6], e[8 * q + 7]));
+            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
           }
           // As a tree: a column with p near 1 then meets the small rest in 13
-          // additions per tile, not in one for each of them (a loss of 1e-5 is
-          // the difference of the sum from 1).
+          // additions at most per segment, not in one for each of them (a loss of
+          // 1e-5 is the difference of the sum from 1).
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
             for (int j = 0; j < d; ++j) e[j] += e[j + d];
           sum += e[0];
         }
-        if (p.e && live && nt == g.ntiles - 1)  // the pitch may reach past the last tile
-          for (int64_t col = n0 + g.bn; col < p.lde; col += 8)
-            *reinterpret_cast<uint4*>(erow + (col - n0)) = make_uint4(0u, 0u, 0u, 0u);
+        if (p.e && live && h == 1 && nt == g.ntiles - 1)  // the pitch may reach past the last tile
+          for (int64_t col = cwidth; n0 + col < p.lde; col += 8)
+            *reinterpret_cast<uint4*>(erow + col) = make_uint4(0u, 0u, 0u, 0u);
         if (live)
-          p.part[static_cast<int64_t>(nt) * p.rows + row] =
-              make_float2(mx == -INFINITY ? mx : ref, sum);
+          p.part[(2 * static_cast<int64_t>(nt) + h) * p.rows + row] = make_float2(mx == -INFINITY ? mx : ref, sum);
         // Target logits: the warp visits the columns that any of its rows wants,
-        // in ascending order (at most bn of them, usually none or a few).
+        // in ascending order (at most a segment of them, usually none or a few).
         int cur = 0, end = 0, want = kNoTarget;
         if (live) {
           if (p.labels) {
@@ -353,7 +405,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               end = 1;
             }
           } else {
-            const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.ntiles + 1) + nt;
+            const uint16_t* o = p.off + static_cast<int64_t>(row) * (2 * g.ntiles + 1) + 2 * nt + h;
             cur = o[0];
             end = o[1];
             if (cur < end) want = p.sidx[static_cast<int64_t>(row) * p.k + cur];
@@ -365,7 +417,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t v = tmem_ld_one(acc + (c - n0));
           tmem_ld_wait();
           if (want == c) {
-            p.ztgt[static_cast<int64_t>(row) * p.k + cur] = __uint_as_float(v) * p.c;
+            p.ztgt[static_cast<int64_t>(row) * p.k + cur] =
+                make_float2(fmaf(__uint_as_float(v), p.c, -ref), ref);
             ++cur;
             want = cur < end ? p.sidx[static_cast<int64_t>(row) * p.k + cur] : kNoTarget;
           }
@@ -373,15 +426,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (MODE == 1 && row0 < p.rows) {
         const bool live = row < p.rows;
-        const float f = live && tail < 0 ? p.rscale[row] : 0.0f;
+        const float2 f = live && tail < 0 ? p.rscale[row] : make_float2(0.0f, 0.0f);
 #pragma unroll 1
-        for (int col = 0; col < TN && n0 + col < p.cols; col += 32) {
+        for (int col = 0; col < cwidth && n0 + col < p.cols; col += 32) {
           uint32_t v[32];
           tmem_ld_32x32b_x32(acc + col, v);
           tmem_ld_wait();
           if (tail >= 0) {  // a piece of a split tile: fp32 sums, joined by k_head_join
             float4* dst = reinterpret_cast<float4*>(
-                p.split + ((static_cast<int64_t>(tail) * g.nsplit + z) * TM + rank * UM + quad * 32 + lane) * TN + col);
+                p.split +
+                ((static_cast<int64_t>(tail) * g.nsplit + z) * TM + rank * UM + quad * 32 + lane) * g.tn + cseg + col);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
@@ -389,7 +443,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           } else if (live) {
             float x[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = f == 0.0f ? 0.0f : __uint_as_float(v[j]) * f;
+            for (int j = 0; j < 32; ++j) x[j] = f.y == 0.0f ? 0.0f : __uint_as_float(v[j]) * f.x * f.y;
             uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n0 + col);
 #pragma unroll
             for (int q = 0; q < 4; ++q)  // cols % 64 == 0: a group of 32 columns is whole
@@ -401,8 +455,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (leader) mbar_arrive(acc_empty(t & 1));
-        else mbar_arrive_remote(empty_at_leader + 8u * (t & 1));
+        if (leader) mbar_arrive(acc_empty(a));
+        else mbar_arrive_remote(empty_at_leader + 8u * a);
       }
     }
   }
@@ -434,38 +488,38 @@ __global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ spl
   pdl_trigger();
   pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  constexpr int per_tile = TM * (TN / 8);
+  const int groups = g.tn / 8, per_tile = TM * groups;
   const int t = static_cast<int>(i / per_tile), w = static_cast<int>(i % per_tile);
   if (t >= g.ntail) return;
-  const int r = w / (TN / 8), c = (w % (TN / 8)) * 8;
+  const int r = w / groups, c = (w % groups) * 8;
   int mt, nt;
   tile_of(g, g.nwhole + t, mt, nt);
-  const int row = mt * TM + r, n = nt * TN + c;
+  const int row = mt * TM + r, n = nt * g.tn + c;
   if (row >= p.rows || n >= p.cols) return;
-  const float* src = split + (static_cast<int64_t>(t) * g.nsplit * TM + r) * TN + c;
+  const float* src = split + (static_cast<int64_t>(t) * g.nsplit * TM + r) * g.tn + c;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
   for (int z = 0; z < g.nsplit; ++z) {
     const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
     a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
     b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
-    src += TM * TN;
+    src += TM * g.tn;
   }
-  const float f = p.rscale[row];
+  const float2 f = p.rscale[row];
   uint4 o = make_uint4(0u, 0u, 0u, 0u);
-  if (f != 0.0f)
-    o = make_uint4(bf16x2_bits(a.x * f, a.y * f), bf16x2_bits(a.z * f, a.w * f), bf16x2_bits(b.x * f, b.y * f),
-                   bf16x2_bits(b.z * f, b.w * f));
+  if (f.y != 0.0f)
+    o = make_uint4(bf16x2_bits(a.x * f.x * f.y, a.y * f.x * f.y), bf16x2_bits(a.z * f.x * f.y, a.w * f.x * f.y),
+                   bf16x2_bits(b.x * f.x * f.y, b.y * f.x * f.y), bf16x2_bits(b.z * f.x * f.y, b.w * f.x * f.y));
   *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n) = o;
 }
 
 // The teacher's slots of one row per block: the softmax of the kept logits over
 // T (as logarithms), in ascending order of their vocabulary index (ties in slot
-// order), and where each vocabulary tile's targets begin.  A slot whose index
+// order), and where each column segment's targets begin.  A slot whose index
 // is outside [0, N) or whose logit is -inf holds nothing: it sorts last.  k is
 // at most 256, so each thread ranks its slot by comparing it with the others.
 template <typename T>
 __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict__ idx, const T* __restrict__ logit,
-                                                      int k, int N, float inv_t, int bn, int ntiles,
+                                                      int k, int N, float inv_t, int tn, int sw, int nseg,
                                                       int* __restrict__ sidx, float* __restrict__ logq,
                                                       uint16_t* __restrict__ off) {
   pdl_trigger();
@@ -497,15 +551,15 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
     logq[row * k + rank] = mine == kNoTarget ? -INFINITY : (val[j] - mx) - lsum;
   }
   __syncthreads();
-  for (int t = s; t <= ntiles; t += blockDim.x) {
-    const int64_t bound = min(static_cast<int64_t>(t) * bn, static_cast<int64_t>(N));
+  for (int t = s; t <= nseg; t += blockDim.x) {
+    const int64_t bound = min(static_cast<int64_t>(t >> 1) * tn + (t & 1) * sw, static_cast<int64_t>(N));
     int lo = 0, hi = k;  // first slot with sorted >= bound
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (sorted[mid] < bound) lo = mid + 1;
       else hi = mid;
     }
-    off[row * (ntiles + 1) + t] = static_cast<uint16_t>(lo);
+    off[row * (nseg + 1) + t] = static_cast<uint16_t>(lo);
   }
 }
 
@@ -514,29 +568,68 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // Factor that takes a sum of exponentials from reference x to reference top.
 __device__ __forceinline__ float shift2(float x, float top) { return x == -INFINITY ? 0.0f : exp2f(x - top); }
 
-// Joins the tiles' (reference, sum) pairs of 32 rows per block: first thread
-// (r, j) takes row r and tiles j, j + 32, ..., then warp r joins its row's 32
-// values and adds up its targets.  The orders are fixed.
+// A row's log2 of the sum of exponentials, m + l2s, and the reference r that its
+// stored exponentials have.  The parts stay apart: their sum would round off
+// digits of z - lse.
+struct RowStat {
+  float m, l2s, r;
+  int rescale;  // some segment is stored relative to its own reference
+};
+
+// Writes p - q, relative to reference r, into the row's target columns (one warp
+// per row).  Cross entropy: p - 1 = expm1(-loss).
+__device__ __forceinline__ void write_targets(uint16_t* er, const RowStat& st, int lane, const int64_t* labels,
+                                              int row, const int* sidx, const float* logq, int k,
+                                              const float2* ztgt) {
+  const float up = exp2f((st.m - st.r) + st.l2s);
+  if (labels) {
+    if (lane == 0) {
+      const float2 z = ztgt[row];
+      const float d = expm1f(((z.x + (z.y - st.m)) - st.l2s) * kLn2) * up;
+      er[labels[row]] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
+    }
+    return;
+  }
+  const int64_t at = static_cast<int64_t>(row) * k;
+  for (int j = lane; j < k; j += 32) {
+    const int y = sidx[at + j];
+    if (y == kNoTarget) break;
+    if (j > 0 && sidx[at + j - 1] == y) continue;  // the first of equal entries takes them all
+    const float2 z = ztgt[at + j];
+    float d = exp2f((z.x + (z.y - st.m)) - st.l2s);
+    for (int o = j; o < k && sidx[at + o] == y; ++o) d -= expf(logq[at + o]);
+    er[y] = static_cast<uint16_t>(bf16x2_bits(d * up, 0.0f));
+  }
+}
+
+// Joins the segments' (reference, sum) pairs of 32 rows per block: first thread
+// (r, j) takes row r and segments j, j + 32, ..., then warp r joins its row's 32
+// values, adds up its targets' terms of the loss and writes its target columns of
+// e.  The orders are fixed.
 __global__ void __launch_bounds__(1024)
-    k_head_stats(const float2* __restrict__ part, int ntiles, int rows, int N, const int64_t* __restrict__ labels,
-                 const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float* __restrict__ ztgt,
+    k_head_stats(const float2* __restrict__ part, int nseg, int rows, int N, const int64_t* __restrict__ labels,
+                 const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float2* __restrict__ ztgt,
                  float temp, const float* __restrict__ dloss, float* __restrict__ loss, float* __restrict__ lse,
-                 float2* __restrict__ lse2, float* __restrict__ rscale) {
+                 RowStat* __restrict__ stat, float2* __restrict__ rscale, uint16_t* __restrict__ e, int64_t lde) {
   pdl_trigger();
   pdl_wait();
   __shared__ float2 sh[32][33];
+  __shared__ bool own[32][33];
   const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
   const int row0 = blockIdx.x * 32;
   float m = -INFINITY, s = 0.0f;
+  bool big = false;
   if (row0 + a < rows) {
-    for (int t = b; t < ntiles; t += 32) {
+    for (int t = b; t < nseg; t += 32) {
       const float2 v = part[static_cast<int64_t>(t) * rows + row0 + a];
       const float top = fmaxf(m, v.x);
       s = s * shift2(m, top) + v.y * shift2(v.x, top);
       m = top;
+      big = big || (fabsf(v.x) > kFits && v.x != -INFINITY);
     }
   }
   sh[b][a] = make_float2(m, s);
+  own[b][a] = big;
   __syncthreads();
   const int row = row0 + b;
   if (row >= rows) return;
@@ -545,85 +638,77 @@ __global__ void __launch_bounds__(1024)
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   s = v.y * shift2(v.x, m);
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  const float l2s = log2f(s);
+  big = __any_sync(0xffffffffu, own[a][b]);
+  const RowStat st{m, log2f(s), big ? m : 0.0f, big ? 1 : 0};
   // loss = T^2 sum_s q_s (log q_s + (lse - z_s)); lse - z_s in units of log2 is
-  // (reference - z_s) + log2(sum), which keeps the digits of a small loss.
+  // (m - n) - (z - n) + log2(sum), which keeps the digits of a small loss.
   float part_loss = 0.0f;
   bool any = false;
   if (labels) {
     const int64_t y = labels[row];
     any = y >= 0 && y < N;
-    if (any && a == 0) part_loss = ((m - ztgt[row]) + l2s) * kLn2;
+    if (any && a == 0) {
+      const float2 z = ztgt[row];
+      part_loss = (((m - z.y) - z.x) + st.l2s) * kLn2;
+    }
   } else {
     const int64_t at = static_cast<int64_t>(row) * k;
     any = sidx[at] != kNoTarget;
     for (int j = a; j < k; j += 32) {
       if (sidx[at + j] == kNoTarget) break;
       const float lq = logq[at + j], q = expf(lq);
-      if (q != 0.0f) part_loss += q * (lq + ((m - ztgt[at + j]) + l2s) * kLn2);
+      const float2 z = ztgt[at + j];
+      if (q != 0.0f) part_loss += q * (lq + (((m - z.y) - z.x) + st.l2s) * kLn2);
     }
   }
   for (int d = 16; d > 0; d >>= 1) part_loss += __shfl_xor_sync(0xffffffffu, part_loss, d);
+  const float g = any ? (dloss ? dloss[row] : 1.0f) * temp : 0.0f;
   if (a == 0) {
     loss[row] = any ? part_loss * (temp * temp) : 0.0f;
-    lse[row] = (m + l2s) * kLn2;
-    if (rscale) {
-      lse2[row] = make_float2(m, l2s);
-      rscale[row] = any ? (dloss ? dloss[row] : 1.0f) * temp : 0.0f;
+    lse[row] = (m + st.l2s) * kLn2;
+    if (e) {
+      stat[row] = st;
+      rscale[row] = make_float2(exp2f(-((m - st.r) + st.l2s)), g);
     }
   }
+  if (e && g != 0.0f && !big)
+    write_targets(e + row * lde, st, a, labels, row, sidx, logq, k, ztgt);
 }
 
 __device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
   return bf16x2_bits(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
 }
 
-// e -> p - q in place: p = e exp2(reference - lse), rounded to bf16 again;
-// target columns hold exp(z - lse) - q from their fp32 logits (cross entropy:
-// expm1, exact where p is near 1).  Block (x, y): row x, the y-th share of its
-// columns (several blocks per row where rows are few, to fill the GPU).
+// Brings the rows that hold a segment with its own reference to the row's common
+// one, then writes their target columns.  A block takes every gridDim.x-th row;
+// usually no row is marked.
 __global__ void __launch_bounds__(256)
-    k_head_scale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int bn, int ntiles, int rows,
-                 const float2* __restrict__ lse2, const float* __restrict__ rscale, const int64_t* __restrict__ labels,
-                 const int* __restrict__ sidx, const float* __restrict__ logq, int k,
-                 const float* __restrict__ ztgt) {
+    k_head_rescale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int tn, int sw, int nseg,
+                   int rows, const RowStat* __restrict__ stat, const float2* __restrict__ rscale,
+                   const int64_t* __restrict__ labels, const int* __restrict__ sidx, const float* __restrict__ logq,
+                   int k, const float2* __restrict__ ztgt) {
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x;
-  if (rscale[row] == 0.0f) return;  // its gradient is written as zeros
-  const float2 l2 = lse2[row];  // subtracted in two steps: their sum would round off digits of z - lse
-  uint16_t* er = e + static_cast<int64_t>(row) * lde;
-  uint4* v = reinterpret_cast<uint4*>(er);
-  const int chunks = static_cast<int>(lde / 8), per_tile = bn / 8;
-  const int share = (chunks + gridDim.y - 1) / gridDim.y;
-  const int c0 = blockIdx.y * share, c1 = min(chunks, c0 + share);
-  for (int c = c0 + threadIdx.x; c < c1; c += 256) {
-    const int t = min(c / per_tile, ntiles - 1);
-    const float f = exp2f(part[static_cast<int64_t>(t) * rows + row].x - l2.x - l2.y);
-    uint4 x = v[c];
-    x.x = scale_pair(x.x, f);
-    x.y = scale_pair(x.y, f);
-    x.z = scale_pair(x.z, f);
-    x.w = scale_pair(x.w, f);
-    v[c] = x;
-  }
-  __syncthreads();
-  const int64_t y0 = 8ll * c0, y1 = 8ll * c1;
-  if (labels) {
-    const int64_t y = labels[row];
-    if (threadIdx.x == 0 && y >= y0 && y < y1) {
-      const float d = expm1f((ztgt[row] - l2.x - l2.y) * kLn2);
-      er[y] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
+  const int chunks = static_cast<int>(lde / 8), per_tile = tn / 8, per_seg = sw / 8;
+  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+    const RowStat st = stat[row];
+    if (!st.rescale || rscale[row].y == 0.0f) continue;
+    uint16_t* er = e + static_cast<int64_t>(row) * lde;
+    uint4* v = reinterpret_cast<uint4*>(er);
+    for (int c = threadIdx.x; c < chunks; c += 256) {
+      const int q = c / per_tile, t = min(2 * q + (c - q * per_tile >= per_seg ? 1 : 0), nseg - 1);
+      const float n = part[static_cast<int64_t>(t) * rows + row].x;
+      const float f = exp2f((fabsf(n) <= kFits ? 0.0f : n) - st.r);
+      uint4 x = v[c];
+      x.x = scale_pair(x.x, f);
+      x.y = scale_pair(x.y, f);
+      x.z = scale_pair(x.z, f);
+      x.w = scale_pair(x.w, f);
+      v[c] = x;
     }
-  } else {
-    const int64_t at = static_cast<int64_t>(row) * k;
-    for (int j = threadIdx.x; j < k; j += 256) {
-      const int y = sidx[at + j];
-      if (y < y0 || y >= y1 || (j > 0 && sidx[at + j - 1] == y)) continue;  // kNoTarget is past every share
-      float d = exp2f(ztgt[at + j] - l2.x - l2.y);
-      for (int o = j; o < k && sidx[at + o] == y; ++o) d -= expf(logq[at + o]);
-      er[y] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
-    }
+    __syncthreads();
+    if (threadIdx.x < 32) write_targets(er, st, threadIdx.x, labels, row, sidx, logq, k, ztgt);
+    __syncthreads();
   }
 }
 
@@ -660,10 +745,10 @@ int head_pairs() {
     cudaLaunchAttribute attr[2];
     int a = 0, b = 0;
     const cudaLaunchConfig_t cfg = pair_config(1, nullptr, attr);
-    if (smem_limit_once<k_head<0>>(SMEM_ALLOC) == cudaSuccess &&
-        smem_limit_once<k_head<1>>(SMEM_ALLOC) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&a, k_head<0>, &cfg) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&b, k_head<1>, &cfg) == cudaSuccess && std::min(a, b) > 0) {
+    if (smem_limit_once<k_head<0, 1>>(SMEM_ALLOC) == cudaSuccess &&
+        smem_limit_once<k_head<1, 1>>(SMEM_ALLOC) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&a, k_head<0, 1>, &cfg) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&b, k_head<1, 1>, &cfg) == cudaSuccess && std::min(a, b) > 0) {
       v = std::min(a, b);
     } else {
       cudaGetLastError();
@@ -709,7 +794,12 @@ HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
       }
     }
   }
-  g.ntiles = static_cast<int>((N + g.bn - 1) / g.bn);
+  static const int env0 = getenv("HNH0") ? atoi(getenv("HNH0")) : 1;
+  g.nh = rows > 256 ? env0 : 1;
+  if (g.nh == 2) g.bn = TN;
+  g.tn = g.nh * g.bn;
+  g.sw = g.nh == 2 ? TN : std::min(g.bn, TN / 2);
+  g.ntiles = static_cast<int>((N + g.tn - 1) / g.tn);
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
   g.band = band_of(g.mtiles, K);
@@ -723,7 +813,11 @@ HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
   HeadGrid g{};
   g.mtiles = static_cast<int>((rows + TM - 1) / TM);
   g.bn = TN;
-  g.ntiles = static_cast<int>((K + TN - 1) / TN);
+  static const int env1 = getenv("HNH1") ? atoi(getenv("HNH1")) : 1;
+  g.nh = rows > 256 && K > 256 ? env1 : 1;
+  g.tn = g.nh * TN;
+  g.sw = g.tn / 2;
+  g.ntiles = static_cast<int>((K + g.tn - 1) / g.tn);
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
   g.band = g.mtiles;
@@ -757,8 +851,9 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct HeadSpace {
   uint16_t* w16;
   float2* part;
-  float2* lse2;  // [rows]: log2 of the sum of exponentials as (largest reference, log2 of the sum relative to it)
-  float *ztgt, *logq, *rscale, *split;
+  float2 *ztgt, *rscale;
+  RowStat* stat;
+  float *logq, *split;
   int* sidx;
   uint16_t *off, *e;
   size_t bytes;
@@ -775,20 +870,20 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
   };
   const HeadGrid g = logits_grid(rows, N, K);
   if (nf4) s.w16 = static_cast<uint16_t*>(take(static_cast<size_t>(N) * K * 2));
-  s.part = static_cast<float2*>(take(static_cast<size_t>(g.ntiles) * rows * 8));
-  s.ztgt = static_cast<float*>(take(static_cast<size_t>(rows) * k * 4));
+  s.part = static_cast<float2*>(take(static_cast<size_t>(2 * g.ntiles) * rows * 8));
+  s.ztgt = static_cast<float2*>(take(static_cast<size_t>(rows) * k * 8));
   if (distill) {
     s.sidx = static_cast<int*>(take(static_cast<size_t>(rows) * k * 4));
     s.logq = static_cast<float*>(take(static_cast<size_t>(rows) * k * 4));
-    s.off = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * (g.ntiles + 1) * 2));
+    s.off = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * (2 * g.ntiles + 1) * 2));
   }
   if (grad) {
-    s.lse2 = static_cast<float2*>(take(static_cast<size_t>(rows) * 8));
-    s.rscale = static_cast<float*>(take(static_cast<size_t>(rows) * 4));
+    s.stat = static_cast<RowStat*>(take(static_cast<size_t>(rows) * sizeof(RowStat)));
+    s.rscale = static_cast<float2*>(take(static_cast<size_t>(rows) * 8));
     s.e = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * e_pitch(N) * 2));
     const HeadGrid d = grad_grid(rows, N, K), last = grad_grid(M % rows, N, K);
-    const int64_t pieces = std::max(int64_t(d.ntail) * d.nsplit, int64_t(last.ntail) * last.nsplit);
-    s.split = static_cast<float*>(take(static_cast<size_t>(pieces) * TM * TN * 4));
+    const int64_t sums = std::max(int64_t(d.ntail) * d.nsplit * d.tn, int64_t(last.ntail) * last.nsplit * last.tn);
+    s.split = static_cast<float*>(take(static_cast<size_t>(sums) * TM * 4));
   }
   s.bytes = at;
   return s;
@@ -804,18 +899,24 @@ int64_t default_piece(int64_t M, int64_t N, bool grad) {
   return std::max<int64_t>(1, std::min<int64_t>(M, ((M + pieces - 1) / pieces + TM - 1) / TM * TM));
 }
 
-template <int MODE>
-cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, int64_t contraction, const HeadGrid& g,
-                        const HeadEpi& p, cudaStream_t st) {
-  cudaError_t e = smem_limit_once<k_head<MODE>>(SMEM_ALLOC);
+template <int MODE, int NH>
+cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, int64_t contraction, const HeadGrid& g,
+                         const HeadEpi& p, cudaStream_t st) {
+  cudaError_t e = smem_limit_once<k_head<MODE, NH>>(SMEM_ALLOC);
   if (e != cudaSuccess) return e;
   const int64_t items = int64_t(g.nwhole) + int64_t(g.ntail) * g.nsplit;
   int P = head_pairs();
   if (P <= 0) P = std::max(1, device_sm_count() / 2);
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = pair_config(static_cast<int>(std::min<int64_t>(items, P)), st, attr);
-  return cudaLaunchKernelEx(&cfg, k_head<MODE>, a, b, static_cast<int>((contraction + BK - 1) / BK), g, p,
+  return cudaLaunchKernelEx(&cfg, k_head<MODE, NH>, a, b, static_cast<int>((contraction + BK - 1) / BK), g, p,
                             device_status_ptr());
+}
+template <int MODE>
+cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, int64_t contraction, const HeadGrid& g,
+                        const HeadEpi& p, cudaStream_t st) {
+  return g.nh == 2 ? launch_pairs<MODE, 2>(a, b, contraction, g, p, st)
+                   : launch_pairs<MODE, 1>(a, b, contraction, g, p, st);
 }
 
 }  // namespace
@@ -874,33 +975,28 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
       const float inv_t = 1.0f / a.temperature;
       if (a.teacher_bf16)
         err = launch_ex(k_head_targets<__nv_bfloat16>, grid, block, 0, st, true, idx,
-                        static_cast<const __nv_bfloat16*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.bn,
-                        g.ntiles, s.sidx, s.logq, s.off);
+                        static_cast<const __nv_bfloat16*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.tn,
+                        g.sw, 2 * g.ntiles, s.sidx, s.logq, s.off);
       else
         err = launch_ex(k_head_targets<float>, grid, block, 0, st, true, idx,
-                        static_cast<const float*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.bn, g.ntiles,
-                        s.sidx, s.logq, s.off);
+                        static_cast<const float*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.tn, g.sw,
+                        2 * g.ntiles, s.sidx, s.logq, s.off);
       if (err != cudaSuccess) return err;
     }
     err = launch_head<0>(ma, mb, a.K, g, p, st);
     if (err != cudaSuccess) return err;
     err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(1024), 0, st, true,
-                    static_cast<const float2*>(s.part), g.ntiles, p.rows, p.cols, p.labels,
+                    static_cast<const float2*>(s.part), 2 * g.ntiles, p.rows, p.cols, p.labels,
                     static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
-                    static_cast<const float*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
-                    a.lse + r0, s.lse2, s.rscale);
-    if (err != cudaSuccess || !grad) {
-      if (err != cudaSuccess) return err;
-      continue;
-    }
-    // At least 2048 elements per block, and as many blocks per row as give about eight to each SM.
-    const int64_t shares =
-        std::max<int64_t>(1, std::min<int64_t>(lde / 2048, (8ll * device_sm_count() + rows - 1) / rows));
-    err = launch_ex(k_head_scale, dim3(static_cast<unsigned>(rows), static_cast<unsigned>(shares)), dim3(256), 0, st,
-                    true, s.e, lde, static_cast<const float2*>(s.part), g.bn, g.ntiles, p.rows,
-                    static_cast<const float2*>(s.lse2),
-                    static_cast<const float*>(s.rscale), p.labels, static_cast<const int*>(s.sidx),
-                    static_cast<const float*>(s.logq), a.k, static_cast<const float*>(s.ztgt));
+                    static_cast<const float2*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
+                    a.lse + r0, s.stat, s.rscale, s.e, lde);
+    if (err != cudaSuccess) return err;
+    if (!grad) continue;
+    err = launch_ex(k_head_rescale, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 4 * device_sm_count()))),
+                    dim3(256), 0, st, true, s.e, lde, static_cast<const float2*>(s.part), g.tn, g.sw, 2 * g.ntiles,
+                    p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float2*>(s.rscale), p.labels,
+                    static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
+                    static_cast<const float2*>(s.ztgt));
     if (err != cudaSuccess) return err;
     const HeadGrid d = grad_grid(rows, a.N, a.K);
     if (!make_map(&ma, BF16, s.e, lde, rows, lde * 2, BK, d.abox, SW) ||
@@ -914,7 +1010,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     q.split = s.split;
     err = launch_head<1>(ma, mb, a.N, d, q, st);
     if (err == cudaSuccess && d.ntail)
-      err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (TN / 8) / 256))), dim3(256), 0, st,
+      err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (d.tn / 8) / 256))), dim3(256), 0, st,
                       true, static_cast<const float*>(s.split), d, q);
     if (err != cudaSuccess) return err;
   }

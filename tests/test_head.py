@@ -11,9 +11,11 @@ Tolerances.  u = 2^-24 is the fp32 rounding, b = 2^-8 the bf16 one.
    trees of 32 and over the tiles, log2, the product with ln 2) are fewer than
    64 roundings of terms no larger than |z| + |lse| + 1, plus 72 relative
    roundings of a sum of positive terms; the tolerance allows 160 u of that.
- - p is rounded twice to bf16 (e and its product with the tile's factor), a
-   target's p - q once; both carry the logits' 2 D and the fp32 steps of the
-   exponent.  The second product adds fp32 steps over the vocabulary (N / 16 +
+ - p is rounded once to bf16 (as e), and so is a target's p - q; both carry the
+   logits' 2 D and the fp32 steps of the exponent.  Entries of e below 2^-126 are
+   flushed to 0, and e is stored relative to a reference that is at most 2^64
+   above the row's sum (or factors of at least 2^-149 bring a value of at most
+   2^64 to one that is), so an entry of p loses at most 2^-62 by that.  The second product adds fp32 steps over the vocabulary (N / 16 +
    16 truncations, and the pieces of a split tile), and dX is rounded once.
 """
 import ctypes
@@ -63,8 +65,9 @@ def reference(W, X, T, q, idx, entropy, dloss, piece=256):
             p = (z - lse[:, None]).exp()
             t = torch.zeros_like(p).scatter_add_(1, idx[s], q[s])
             g = (T * dloss[s].double() * told)[:, None]
-            dp = p * (2.05 * B16 + (3 * D + 2 * steps)[:, None])  # of the entries that are no targets, and
-            dt = (p - t).abs() * 1.01 * B16 + (p + t) * (3 * D + 2 * steps + 64 * U)[:, None]  # of those that are
+            dp = p * (1.02 * B16 + (3 * D + 2 * steps)[:, None]) + 2.0**-62  # of the entries that are no targets, and
+            dt = (p - t).abs() * 1.01 * B16 + (p + t) * (3 * D + 2 * steps + 64 * U)[:, None]  # of those that are,
+            dt = dt + 2.0**-62  # with what is flushed
             dp = torch.where(t > 0, dt, dp)
             rows = (N / 16 + 16 + 64) * 2 * U * ((p + t) @ W.abs())
             dx = g * ((p - t) @ W)
@@ -246,7 +249,7 @@ def test_confident_tokens_keep_the_digits_of_their_gradient(L):
     """A label with p near 1: loss and p - 1 are small differences, held to their own size.  The sum of exponentials
     is 1 + loss; the label's 1 passes 5 additions in its group of 32, 8 in its tile, 1 + 5 over the tiles and lanes,
     then log2, two products with ln 2 and expm1: 24 fp32 roundings near 1.  The entries of p - q are rounded to bf16
-    twice and dX once."""
+    once and dX once, the row's factors three times in fp32."""
     M, N, K = 64, 500, 256
     g = wl.generator(3)
     W = torch.randn(N, K, generator=g).sign() * 0.125
@@ -260,6 +263,34 @@ def test_confident_tokens_keep_the_digits_of_their_gradient(L):
     rel = (got[2].double() - ref["dx"]).norm(dim=1) / ref["dx"].norm(dim=1)
     assert ref["loss"].min() < 1e-6
     assert (rel <= 24 * U / ref["loss"] + 3 * B16)[ref["loss"] > 1e-5].all()
+
+
+@gpu
+@pytest.mark.parametrize("distill", [False, True])
+def test_logits_of_any_size(L, distill):
+    """Rows whose logits are far from 0: near +-45 (where the stored exponentials change their reference), in the
+    hundreds, all far below 0, and some segments below with others above, next to ordinary rows."""
+    M, N, K = 160, 1400, 256
+    head, values, X, labels, g = make(81, M, N, K, w_std=0.06)
+    W = values.float()
+    W[:, 0] = 1.0                                  # a common offset: X[:, 0]
+    W[:, 1] = (torch.arange(N) // 128 % 2).cuda()  # one of some segments: X[:, 1]
+    head = W.bfloat16()
+    X[:, :2] = 0
+    X[10:40] *= torch.logspace(0, 2, 30).cuda()[:, None].bfloat16()
+    X[40:70, 0] = torch.linspace(30, 300, 30).cuda().bfloat16()
+    X[70:100, 0] = -torch.linspace(30, 300, 30).cuda().bfloat16()
+    X[100:120, 0], X[100:120, 1] = -90, torch.linspace(20, 200, 20).cuda().bfloat16()
+    X[120:140, 1] = torch.linspace(-200, 200, 20).cuda().bfloat16()
+    dloss = torch.rand(M, generator=g).cuda()
+    if distill:
+        idx, t = teacher(g, M, N, 20, False)
+        got = qb.qlora_head_distill(head, X, idx, t, 1.0, dloss=dloss)
+        ref = reference(head, X, 1.0, *distill_targets(idx, t, N, 1.0), dloss)
+    else:
+        got = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+        ref = reference(head, X, 1.0, *xent_targets(labels, N), dloss)
+    compare(got, ref)
 
 
 @gpu
