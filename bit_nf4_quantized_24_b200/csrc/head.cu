@@ -30,7 +30,6 @@
 //    reference, by exact powers of two.
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 
 #include "internal.h"
 
@@ -74,8 +73,8 @@ struct HeadGrid {
   int mtiles, ntiles;         // token tiles of 256, output tiles of tn
   int nwhole, ntail, nsplit;
   int band;                   // token tiles walked together
-  int nh;                     // accumulators per tile, side by side along the outputs
-  int bn;                     // outputs per accumulator (a multiple of 32; 256 if nh = 2 or MODE 1)
+  int nh;                     // accumulators per tile, side by side along the outputs (2 in MODE 1 only)
+  int bn;                     // outputs per accumulator (a multiple of 32; 256 in MODE 1)
   int tn;                     // outputs per tile, nh bn
   int sw;                     // outputs of the first of a tile's two column segments (one per epilogue group)
   int abox;                   // token rows of the A box: UM, or fewer when the whole piece fits one CTA
@@ -290,8 +289,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const uint32_t b_h = b_s + h * B_BYTES;
               const uint64_t bd =
                   MODE == 0 ? desc_sw128(b_h + kk * 32, 16, 1024) : desc_sw128(b_h + kk * 2048, 8192, 1024);
-              tc_mma_f16_pair(d + 256u * h, desc_sw128(a_s + kk * 32, 16, 1024), bd, idesc,
-                              (k > kbeg || kk > 0) ? 1u : 0u);
+              const uint64_t ad = desc_sw128(a_s + kk * 32, 16, 1024);
+              const uint32_t more = (k > kbeg || kk > 0) ? 1u : 0u;
+              if (NH == 1) tc_mma_f16_pair(d, ad, bd, idesc, more);
+              else if (h == 0) tc_mma_f16_pair_fill_a(d, ad, bd, idesc, more);
+              else tc_mma_f16_pair_last_a(d + 256u, ad, bd, idesc, more);
             }
           }
           tc_commit_pair(empty(s));
@@ -498,6 +500,7 @@ __global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ spl
   if (row >= p.rows || n >= p.cols) return;
   const float* src = split + (static_cast<int64_t>(t) * g.nsplit * TM + r) * g.tn + c;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+#pragma unroll 4
   for (int z = 0; z < g.nsplit; ++z) {
     const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
     a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
@@ -602,43 +605,48 @@ __device__ __forceinline__ void write_targets(uint16_t* er, const RowStat& st, i
   }
 }
 
-// Joins the segments' (reference, sum) pairs of 32 rows per block: first thread
-// (r, j) takes row r and segments j, j + 32, ..., then warp r joins its row's 32
+// Joins the segments' (reference, sum) pairs of 8 rows per block: first thread
+// (r, j) takes row r and segments j, j + 64, ..., then warp r joins its row's 64
 // values, adds up its targets' terms of the loss and writes its target columns of
 // e.  The orders are fixed.
-__global__ void __launch_bounds__(1024)
+constexpr int SROWS = 8, SLANES = 64;
+__global__ void __launch_bounds__(SROWS * SLANES)
     k_head_stats(const float2* __restrict__ part, int nseg, int rows, int N, const int64_t* __restrict__ labels,
                  const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float2* __restrict__ ztgt,
                  float temp, const float* __restrict__ dloss, float* __restrict__ loss, float* __restrict__ lse,
                  RowStat* __restrict__ stat, float2* __restrict__ rscale, uint16_t* __restrict__ e, int64_t lde) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float2 sh[32][33];
-  __shared__ bool own[32][33];
-  const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
-  const int row0 = blockIdx.x * 32;
+  __shared__ float2 sh[SROWS][SLANES + 1];
+  __shared__ int own[SROWS];
+  const int row0 = blockIdx.x * SROWS;
   float m = -INFINITY, s = 0.0f;
   bool big = false;
-  if (row0 + a < rows) {
-    for (int t = b; t < nseg; t += 32) {
-      const float2 v = part[static_cast<int64_t>(t) * rows + row0 + a];
+  const int r = threadIdx.x % SROWS, seg0 = threadIdx.x / SROWS;
+  if (threadIdx.x < SROWS) own[threadIdx.x] = 0;
+  __syncthreads();
+  if (row0 + r < rows) {
+#pragma unroll 4
+    for (int t = seg0; t < nseg; t += SLANES) {
+      const float2 v = part[static_cast<int64_t>(t) * rows + row0 + r];
       const float top = fmaxf(m, v.x);
       s = s * shift2(m, top) + v.y * shift2(v.x, top);
       m = top;
       big = big || (fabsf(v.x) > kFits && v.x != -INFINITY);
     }
   }
-  sh[b][a] = make_float2(m, s);
-  own[b][a] = big;
+  sh[r][seg0] = make_float2(m, s);
+  if (big) own[r] = 1;
   __syncthreads();
+  const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
   const int row = row0 + b;
-  if (row >= rows) return;
-  const float2 v = sh[a][b];
-  m = v.x;
+  if (b >= SROWS || row >= rows) return;
+  const float2 v = sh[b][a], w = sh[b][a + 32];
+  m = fmaxf(v.x, w.x);
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  s = v.y * shift2(v.x, m);
+  s = v.y * shift2(v.x, m) + w.y * shift2(w.x, m);
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  big = __any_sync(0xffffffffu, own[a][b]);
+  big = own[b] != 0;
   const RowStat st{m, log2f(s), big ? m : 0.0f, big ? 1 : 0};
   // loss = T^2 sum_s q_s (log q_s + (lse - z_s)); lse - z_s in units of log2 is
   // (m - n) - (z - n) + log2(sum), which keeps the digits of a small loss.
@@ -681,7 +689,7 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
 
 // Brings the rows that hold a segment with its own reference to the row's common
 // one, then writes their target columns.  A block takes every gridDim.x-th row;
-// usually no row is marked.
+// usually no row is marked, which its threads see in one look at 256 of them.
 __global__ void __launch_bounds__(256)
     k_head_rescale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int tn, int sw, int nseg,
                    int rows, const RowStat* __restrict__ stat, const float2* __restrict__ rscale,
@@ -691,6 +699,13 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   const int chunks = static_cast<int>(lde / 8), per_tile = tn / 8, per_seg = sw / 8;
   for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+    if ((row - static_cast<int>(blockIdx.x)) % (256 * static_cast<int>(gridDim.x)) == 0) {
+      const int64_t mine = row + static_cast<int64_t>(threadIdx.x) * gridDim.x;
+      if (!__syncthreads_or(mine < rows && stat[mine].rescale)) {
+        row += 255 * gridDim.x;
+        continue;
+      }
+    }
     const RowStat st = stat[row];
     if (!st.rescale || rscale[row].y == 0.0f) continue;
     uint16_t* er = e + static_cast<int64_t>(row) * lde;
@@ -794,11 +809,9 @@ HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
       }
     }
   }
-  static const int env0 = getenv("HNH0") ? atoi(getenv("HNH0")) : 1;
-  g.nh = rows > 256 ? env0 : 1;
-  if (g.nh == 2) g.bn = TN;
-  g.tn = g.nh * g.bn;
-  g.sw = g.nh == 2 ? TN : std::min(g.bn, TN / 2);
+  g.nh = 1;
+  g.tn = g.bn;
+  g.sw = std::min(g.bn, TN / 2);
   g.ntiles = static_cast<int>((N + g.tn - 1) / g.tn);
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
@@ -807,15 +820,15 @@ HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
   return g;
 }
 
-// Tiles of the gradient product; the tiles of a partial last wave are split
-// along the vocabulary.
-HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
+// Tiles of the gradient product of width 256 nh; the tiles of a partial last
+// wave are split along the vocabulary where that saves time.  *cost: estimated
+// time in stages of a 256-wide tile.
+HeadGrid grad_tiles(int64_t rows, int64_t N, int64_t K, int nh, double* cost) {
   HeadGrid g{};
   g.mtiles = static_cast<int>((rows + TM - 1) / TM);
   g.bn = TN;
-  static const int env1 = getenv("HNH1") ? atoi(getenv("HNH1")) : 1;
-  g.nh = rows > 256 && K > 256 ? env1 : 1;
-  g.tn = g.nh * TN;
+  g.nh = nh;
+  g.tn = nh * TN;
   g.sw = g.tn / 2;
   g.ntiles = static_cast<int>((K + g.tn - 1) / g.tn);
   g.nwhole = g.mtiles * g.ntiles;
@@ -824,25 +837,38 @@ HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
   g.abox = a_box(rows);
   const int64_t numK = (N + BK - 1) / BK;
   const int P = head_pairs();
+  *cost = 0.0;
   if (P <= 0) return g;
-  const int64_t w = g.nwhole % P;
-  if (w == 0) return g;
-  int64_t S = 1;
-  double best = 0.0;
-  for (int64_t c = 2; c <= std::min<int64_t>(numK / 8, 64); ++c) {
-    const double rounds = static_cast<double>((w * c + P - 1) / P);
-    const double save = (1.0 - rounds / static_cast<double>(c)) * static_cast<double>(numK) - 0.1 * w * c;
-    if (save > best) {
-      best = save;
-      S = c;
+  // Two accumulators side by side bring 48 KB per CTA for twice the products of
+  // 32 KB: 2.79 against 2.99 ms for 2048 x 128000 x 8192, where both divide the
+  // pairs alike.
+  const double stage = nh == 2 ? 1.87 : 1.0;
+  const int64_t w = g.nwhole % P, full = g.nwhole / P;
+  double tail = w ? static_cast<double>(numK) * stage : 0.0;
+  // Split in S, the w tiles of the last wave take ceil(w S / P) rounds of S-ths;
+  // their fp32 sums (256 KB per piece and accumulator, written and read again)
+  // cost about 0.2 of a stage each, and every round the filling and emptying of
+  // the pipeline.
+  for (int64_t S = 2; w && S <= std::min<int64_t>(numK / 8, 64); ++S) {
+    const double rounds = static_cast<double>((w * S + P - 1) / P);
+    const double t = rounds / static_cast<double>(S) * static_cast<double>(numK) * stage +
+                     0.2 * nh * static_cast<double>(w * S) + 8.0 * nh * rounds;
+    if (t < tail) {
+      tail = t;
+      g.nsplit = static_cast<int>(S);
     }
   }
-  if (S > 1) {
-    g.nsplit = static_cast<int>(S);
+  if (g.nsplit > 1) {
     g.ntail = static_cast<int>(w);
     g.nwhole -= g.ntail;
   }
+  *cost = static_cast<double>(full) * static_cast<double>(numK) * stage + tail;
   return g;
+}
+HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
+  double one = 0.0, two = 0.0;
+  const HeadGrid a = grad_tiles(rows, N, K, 1, &one), b = grad_tiles(rows, N, K, 2, &two);
+  return two < one ? b : a;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -890,11 +916,11 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
 }
 
 // Tokens per piece when the caller leaves the choice to the library: with a
-// gradient e takes at most 512 MB, without one the tiles' statistics are small
+// gradient e takes at most 1 GB, without one the tiles' statistics are small
 // and 16384 tokens go at once.  Pieces of a call are alike, in whole tiles.
 int64_t default_piece(int64_t M, int64_t N, bool grad) {
   const int64_t most =
-      grad ? std::max<int64_t>(TM, (512ll << 20) / (e_pitch(N) * 2) / TM * TM) : int64_t(64) * TM;
+      grad ? std::max<int64_t>(TM, (1ll << 30) / (e_pitch(N) * 2) / TM * TM) : int64_t(64) * TM;
   const int64_t pieces = std::max<int64_t>(1, (M + most - 1) / most);
   return std::max<int64_t>(1, std::min<int64_t>(M, ((M + pieces - 1) / pieces + TM - 1) / TM * TM));
 }
@@ -912,13 +938,6 @@ cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, int64_t con
   return cudaLaunchKernelEx(&cfg, k_head<MODE, NH>, a, b, static_cast<int>((contraction + BK - 1) / BK), g, p,
                             device_status_ptr());
 }
-template <int MODE>
-cudaError_t launch_head(const CUtensorMap& a, const CUtensorMap& b, int64_t contraction, const HeadGrid& g,
-                        const HeadEpi& p, cudaStream_t st) {
-  return g.nh == 2 ? launch_pairs<MODE, 2>(a, b, contraction, g, p, st)
-                   : launch_pairs<MODE, 1>(a, b, contraction, g, p, st);
-}
-
 }  // namespace
 
 size_t head_workspace_bytes(int64_t piece, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad,
@@ -983,9 +1002,10 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
                         2 * g.ntiles, s.sidx, s.logq, s.off);
       if (err != cudaSuccess) return err;
     }
-    err = launch_head<0>(ma, mb, a.K, g, p, st);
+    err = launch_pairs<0, 1>(ma, mb, a.K, g, p, st);
     if (err != cudaSuccess) return err;
-    err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(1024), 0, st, true,
+    err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
+                    true,
                     static_cast<const float2*>(s.part), 2 * g.ntiles, p.rows, p.cols, p.labels,
                     static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
                     static_cast<const float2*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
@@ -1008,7 +1028,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     q.rscale = s.rscale;
     q.out = a.dX + r0 * a.K;
     q.split = s.split;
-    err = launch_head<1>(ma, mb, a.N, d, q, st);
+    err = d.nh == 2 ? launch_pairs<1, 2>(ma, mb, a.N, d, q, st) : launch_pairs<1, 1>(ma, mb, a.N, d, q, st);
     if (err == cudaSuccess && d.ntail)
       err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (d.tn / 8) / 256))), dim3(256), 0, st,
                       true, static_cast<const float*>(s.split), d, q);

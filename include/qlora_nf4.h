@@ -371,7 +371,7 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  * workspace: qlora_head_workspace bytes, 256-byte aligned.  Tokens are taken
  * in pieces; with a gradient the workspace holds M' x N bf16 values for a piece
  * of M' tokens.  piece = 0 asks for the bytes of the library's own choice (at
- * most 512 MB of such values), another piece for at most that many tokens at
+ * most 1 GB of such values), another piece for at most that many tokens at
  * a time; the calls use the largest pieces that fit the workspace they get,
  * down to 256 tokens (or M, if fewer), below which they return
  * QLORA_ERR_WORKSPACE.  k = 0 asks for qlora_head_xent, k >= 1 for

@@ -491,7 +491,7 @@ def test_workspace_sizes(L):
     assert a % 256 == 0 and a >= 4096 * 32000 * 2
     assert qb.head_workspace_bytes(4096, 32000, 4096, want_dx=False) < a // 16  # no logits, no exponentials
     assert qb.head_workspace_bytes(4096, 32000, 4096, piece=256) < a // 8
-    assert qb.head_workspace_bytes(1 << 20, 128000, 4096) < (1 << 30)  # bounded however many tokens there are
+    assert qb.head_workspace_bytes(1 << 20, 128000, 4096) < (3 << 29)  # bounded however many tokens there are
     assert qb.head_workspace_bytes(4096, 32000, 4096, nf4=True) >= a + 32000 * 4096 * 2
     assert qb.head_workspace_bytes(4096, 32000, 4096, k=64) > a
     assert qb.head_workspace_bytes(0, 32000, 4096) > 0
