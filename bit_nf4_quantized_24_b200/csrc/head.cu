@@ -45,9 +45,11 @@ constexpr int A_BYTES = UM * BK * 2;
 constexpr int B_BYTES = TN / 2 * BK * 2;  // per accumulator
 constexpr int RING_BYTES = 192 * 1024;    // 6 stages of 32 KB (NH = 1) or 4 of 48 KB (NH = 2)
 constexpr int MAX_STAGES = 6;
-constexpr int OFF_BAR = RING_BYTES;
-constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignment
 constexpr int EPI_WARPS = 8;
+constexpr int E_BYTES = 32 * 64;          // 32 rows of 32 bf16 on their way out, two buffers per warp
+constexpr int OFF_E = RING_BYTES;
+constexpr int OFF_BAR = OFF_E + EPI_WARPS * 2 * E_BYTES;
+constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignment
 constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int kNoTarget = 0x7fffffff;
@@ -73,8 +75,8 @@ struct HeadGrid {
   int mtiles, ntiles;         // token tiles of 256, output tiles of tn
   int nwhole, ntail, nsplit;
   int band;                   // token tiles walked together
-  int nh;                     // accumulators per tile, side by side along the outputs (2 in MODE 1 only)
-  int bn;                     // outputs per accumulator (a multiple of 32; 256 in MODE 1)
+  int nh;                     // accumulators per tile, side by side along the outputs
+  int bn;                     // outputs per accumulator (a multiple of 32; 256 if nh = 2 or MODE 1)
   int tn;                     // outputs per tile, nh bn
   int sw;                     // outputs of the first of a tile's two column segments (one per epilogue group)
   int abox;                   // token rows of the A box: UM, or fewer when the whole piece fits one CTA
@@ -140,8 +142,8 @@ struct HeadEpi {
 // it issued, frees TMEM and returns.
 template <int MODE, int NH>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    k_head(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int numK, HeadGrid g,
-           HeadEpi p, int* status) {
+    k_head(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+           const __grid_constant__ CUtensorMap tm_e, int numK, HeadGrid g, HeadEpi p, int* status) {
   constexpr int STAGE_BYTES = A_BYTES + NH * B_BYTES;
   constexpr int STAGES = RING_BYTES / STAGE_BYTES;
   static_assert(STAGES <= MAX_STAGES, "barrier block");
@@ -321,7 +323,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t empty_at_leader = mapa_shared(acc_empty(0), 0);
     const int cseg = h * g.sw;                         // the segment's first column in the tile
     const int cwidth = h == 0 ? g.sw : g.tn - g.sw;    // and its width
-    int t = 0;
+    const uint32_t e_buf = base + OFF_E + static_cast<uint32_t>(warp - 2) * 2 * E_BYTES;
+    int t = 0, stored = 0;
     for (int i = first; i < nitems; i += step, ++t) {
       int mt, nt, kbeg, kend, tail, z;
       item(i, mt, nt, kbeg, kend, tail, z);
@@ -358,7 +361,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float back = exp2f(fabsf(ref) <= kFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
         const __nv_bfloat162 back2 = __float2bfloat162_rn(back);
         float sum = 0.0f;
-        uint16_t* erow = p.e ? p.e + static_cast<int64_t>(row) * p.lde + n0 : nullptr;
         const int ewidth = static_cast<int>(min(static_cast<int64_t>(cwidth), p.lde - n0));
 #pragma unroll 1
         for (int col = 0; col < ewidth; col += 32) {
@@ -371,16 +373,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), p.c, -ref));
             if (col + 32 > ncols && col + j >= ncols) e[j] = 0.0f;
           }
-          if (p.e && live) {
-            uint32_t w[16];
+          if (p.e) {
+            // 32 rows x 32 columns through shared memory (64-byte swizzle) and out by
+            // TMA: written from the registers, every 16 bytes of a lane would be a
+            // line of their own.  Rows past the piece are not written.
+            const uint32_t buf = e_buf + static_cast<uint32_t>(stored & 1) * E_BYTES;
+            if (lane == 0) bulk_wait_read<1>();  // the store before the last has left this buffer
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 x = __hmul2(__floats2bfloat162_rn(e[2 * j], e[2 * j + 1]), back2);
-              w[j] = *reinterpret_cast<const uint32_t*>(&x);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 x = __hmul2(__floats2bfloat162_rn(e[8 * q + 2 * j], e[8 * q + 2 * j + 1]), back2);
+                w[j] = *reinterpret_cast<const uint32_t*>(&x);
+              }
+              st_shared_v4(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
             }
-            uint4* dst = reinterpret_cast<uint4*>(erow + col);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tm_e, buf, n0 + col, row0);
+              bulk_commit();
+            }
+            ++stored;
           }
           // As a tree: a column with p near 1 then meets the small rest in 13
           // additions at most per segment, not in one for each of them (a loss of
@@ -392,8 +408,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           sum += e[0];
         }
         if (p.e && live && h == 1 && nt == g.ntiles - 1)  // the pitch may reach past the last tile
-          for (int64_t col = cwidth; n0 + col < p.lde; col += 8)
-            *reinterpret_cast<uint4*>(erow + col) = make_uint4(0u, 0u, 0u, 0u);
+          for (int64_t col = n0 + cwidth; col < p.lde; col += 8)
+            *reinterpret_cast<uint4*>(p.e + static_cast<int64_t>(row) * p.lde + col) = make_uint4(0u, 0u, 0u, 0u);
         if (live)
           p.part[(2 * static_cast<int64_t>(nt) + h) * p.rows + row] = make_float2(mx == -INFINITY ? mx : ref, sum);
         // Target logits: the warp visits the columns that any of its rows wants,
@@ -461,6 +477,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         else mbar_arrive_remote(empty_at_leader + 8u * a);
       }
     }
+    if (MODE == 0 && lane == 0) bulk_wait_all();  // the stores have left shared memory and are visible
   }
 
   // Both CTAs must be done with the pair's TMEM, and with each other's
@@ -792,12 +809,16 @@ int a_box(int64_t rows) { return rows < UM ? static_cast<int>((rows + 7) / 8 * 8
 // per CTA are 64 B per cycle, about what L2 delivers, so narrower tiles only pay
 // where they save a round.  With a single token tile the head's rows alone count
 // (they come from HBM): 32000 entries are two rounds of 256 on 74 pairs, or two
-// of 224.
+// of 224.  A tile of 512 (two accumulators, whose epilogue no other tile's
+// products cover) takes 0.913 of the time per stage and about 7 stages more per
+// 256 outputs: measured 0.97 of the time at K = 8192, 1.02 at 4096.
 HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
   HeadGrid g{};
   g.mtiles = static_cast<int>((rows + TM - 1) / TM);
   g.bn = TN;
   const int P = head_pairs();
+  const double numK = static_cast<double>((K + BK - 1) / BK);
+  g.nh = 1;
   if (P > 0) {
     double best = 0.0;
     for (int bn = TN; bn >= 128; bn -= 32) {
@@ -808,10 +829,15 @@ HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
         g.bn = bn;
       }
     }
+    const int64_t rounds = (g.mtiles * ((N + 2 * TN - 1) / (2 * TN)) + P - 1) / P;
+    const double cost = static_cast<double>(rounds) * TN * 2 * (0.913 + 6.8 / numK);
+    if (g.mtiles > 1 && cost < best) {
+      g.nh = 2;
+      g.bn = TN;
+    }
   }
-  g.nh = 1;
-  g.tn = g.bn;
-  g.sw = std::min(g.bn, TN / 2);
+  g.tn = g.nh * g.bn;
+  g.sw = g.nh == 2 ? TN : std::min(g.bn, TN / 2);
   g.ntiles = static_cast<int>((N + g.tn - 1) / g.tn);
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
@@ -926,8 +952,8 @@ int64_t default_piece(int64_t M, int64_t N, bool grad) {
 }
 
 template <int MODE, int NH>
-cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, int64_t contraction, const HeadGrid& g,
-                         const HeadEpi& p, cudaStream_t st) {
+cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, int64_t contraction,
+                         const HeadGrid& g, const HeadEpi& p, cudaStream_t st) {
   cudaError_t e = smem_limit_once<k_head<MODE, NH>>(SMEM_ALLOC);
   if (e != cudaSuccess) return e;
   const int64_t items = int64_t(g.nwhole) + int64_t(g.ntail) * g.nsplit;
@@ -935,7 +961,7 @@ cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, int64_t con
   if (P <= 0) P = std::max(1, device_sm_count() / 2);
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = pair_config(static_cast<int>(std::min<int64_t>(items, P)), st, attr);
-  return cudaLaunchKernelEx(&cfg, k_head<MODE, NH>, a, b, static_cast<int>((contraction + BK - 1) / BK), g, p,
+  return cudaLaunchKernelEx(&cfg, k_head<MODE, NH>, a, b, out, static_cast<int>((contraction + BK - 1) / BK), g, p,
                             device_status_ptr());
 }
 }  // namespace
@@ -972,9 +998,10 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     const int64_t rows = std::min(a.piece, a.M - r0);
     const HeadGrid g = logits_grid(rows, a.N, a.K);
     const uint16_t* X = a.X + r0 * a.K;
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, me{};  // me: e as the logits product writes it
     if (!make_map(&ma, BF16, X, a.K, rows, a.K * 2, BK, g.abox, SW) ||
-        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, BK, g.bn / 2, SW))
+        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, BK, g.bn / 2, SW) ||
+        (grad && !make_map(&me, BF16, s.e, lde, rows, lde * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
       return cudaErrorInvalidValue;
     HeadEpi p{};
     p.rows = static_cast<int>(rows);
@@ -1002,7 +1029,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
                         2 * g.ntiles, s.sidx, s.logq, s.off);
       if (err != cudaSuccess) return err;
     }
-    err = launch_pairs<0, 1>(ma, mb, a.K, g, p, st);
+    err = g.nh == 2 ? launch_pairs<0, 2>(ma, mb, me, a.K, g, p, st) : launch_pairs<0, 1>(ma, mb, me, a.K, g, p, st);
     if (err != cudaSuccess) return err;
     err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
                     true,
@@ -1028,7 +1055,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     q.rscale = s.rscale;
     q.out = a.dX + r0 * a.K;
     q.split = s.split;
-    err = d.nh == 2 ? launch_pairs<1, 2>(ma, mb, a.N, d, q, st) : launch_pairs<1, 1>(ma, mb, a.N, d, q, st);
+    err = d.nh == 2 ? launch_pairs<1, 2>(ma, mb, me, a.N, d, q, st) : launch_pairs<1, 1>(ma, mb, me, a.N, d, q, st);
     if (err == cudaSuccess && d.ntail)
       err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (d.tn / 8) / 256))), dim3(256), 0, st,
                       true, static_cast<const float*>(s.split), d, q);
