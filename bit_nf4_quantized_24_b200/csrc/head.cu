@@ -31,7 +31,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "internal.h"
+#include "head.h"
 
 namespace qn {
 
@@ -53,7 +53,6 @@ constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignme
 constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int kNoTarget = 0x7fffffff;
-constexpr float kFits = 64.0f;  // |reference| (log2) up to which e is stored without it
 
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 
@@ -79,7 +78,6 @@ struct HeadGrid {
   int bn;                     // outputs per accumulator (a multiple of 32; 256 if nh = 2 or MODE 1)
   int tn;                     // outputs per tile, nh bn
   int sw;                     // outputs of the first of a tile's two column segments (one per epilogue group)
-  int abox;                   // token rows of the A box: UM, or fewer when the whole piece fits one CTA
 };
 
 __device__ __forceinline__ void tile_of(const HeadGrid& g, int L, int& mt, int& nt) {
@@ -90,39 +88,11 @@ __device__ __forceinline__ void tile_of(const HeadGrid& g, int L, int& mt, int& 
   mt = b * g.band + (rem - nt * in_band);
 }
 
-// exp2 on the special-function unit: relative error about 2^-22, which is far
-// below the bf16 rounding of e and of the order of the fp32 sums' own rounding.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t tmem_ld_one(uint32_t taddr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
   return r;
 }
-
-// What the epilogues read and write (MODE 0: logits, MODE 1: gradient).
-struct HeadEpi {
-  int rows;         // token rows of the piece
-  int cols;         // MODE 0: N; MODE 1: K
-  // MODE 0
-  float c;                   // log2(e) / T
-  float2* part;              // [2 ntiles][rows], per column segment: (reference n, sum of exp2(z c - n))
-  uint16_t* e;               // [rows][lde] (nullable)
-  int64_t lde;
-  const int64_t* labels;     // [rows] (cross entropy), or
-  const int* sidx;           // [rows][k] targets in ascending order, and
-  const uint16_t* off;       // [rows][2 ntiles + 1] first target of each column segment
-  int k;
-  float2* ztgt;              // [rows][k] target logits: (z c - n, n)
-  // MODE 1
-  const float2* rscale;      // [rows] factors (x, y) of the row (y = 0: the row is written as zeros)
-  uint16_t* out;             // [rows][cols]
-  float* split;              // fp32 sums of the split tiles' pieces
-};
 
 // D = A B^T by pairs of CTAs (cta_group::2): 256 tokens x NH accumulators of up
 // to 256 outputs per tile, each CTA holding 128 token rows and half of the
@@ -205,12 +175,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
   }
-  if (g.abox < UM) {  // the rows that no copy writes hold zeros
-    for (int s = 0; s < STAGES; ++s)
-      for (int i = threadIdx.x; i < A_BYTES / 16; i += NUM_THREADS)
-        st_shared_v4(base + s * STAGE_BYTES + 16 * i, 0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
-  }
   if (warp == 1) {
     tmem_alloc_pair(bar0 + static_cast<uint32_t>(offsetof(HeadBars, tmem_base)), TMEM_COLS);
     tmem_relinquish_pair();
@@ -224,8 +188,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     // --------------------------------------------------------- TMA producer
     if (lane == 0) {
-      const bool one = g.abox < UM;  // all tokens in the leader's rows, of which abox are loaded
-      const uint32_t bytes = ((one ? 1 : 2) * g.abox + 2 * NH * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
+      const uint32_t bytes = 2 * (UM + NH * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
       const uint32_t full_at_leader = mapa_shared(full(0), 0);
       bool ok = true;
       int n = 0;  // stages issued
@@ -238,7 +201,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!(ok = wait_bounded(empty(s), ((n / STAGES) & 1) ^ 1, abort, status))) break;
           if (leader) mbar_arrive_expect_tx(full(s), bytes);
           const uint32_t bar = full_at_leader + 8u * s, a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
-          if (!one || leader) tma_load_2d_pair(a_s, &tm_a, bar, k * BK, m0);
+          tma_load_2d_pair(a_s, &tm_a, bar, k * BK, m0);
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             if (MODE == 0) {
@@ -358,7 +321,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // off and putting it back are exact.  (A segment whose logits are all -inf
         // or NaN is summed around 0.)
         const float ref = mx == -INFINITY ? 0.0f : rintf(mx * p.c);
-        const float back = exp2f(fabsf(ref) <= kFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
+        const float back = exp2f(fabsf(ref) <= kHeadFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
         const __nv_bfloat162 back2 = __float2bfloat162_rn(back);
         float sum = 0.0f;
         const int ewidth = static_cast<int>(min(static_cast<int64_t>(cwidth), p.lde - n0));
@@ -649,7 +612,7 @@ __global__ void __launch_bounds__(SROWS * SLANES)
       const float top = fmaxf(m, v.x);
       s = s * shift2(m, top) + v.y * shift2(v.x, top);
       m = top;
-      big = big || (fabsf(v.x) > kFits && v.x != -INFINITY);
+      big = big || (fabsf(v.x) > kHeadFits && v.x != -INFINITY);
     }
   }
   sh[r][seg0] = make_float2(m, s);
@@ -730,7 +693,7 @@ __global__ void __launch_bounds__(256)
     for (int c = threadIdx.x; c < chunks; c += 256) {
       const int q = c / per_tile, t = min(2 * q + (c - q * per_tile >= per_seg ? 1 : 0), nseg - 1);
       const float n = part[static_cast<int64_t>(t) * rows + row].x;
-      const float f = exp2f((fabsf(n) <= kFits ? 0.0f : n) - st.r);
+      const float f = exp2f((fabsf(n) <= kHeadFits ? 0.0f : n) - st.r);
       uint4 x = v[c];
       x.x = scale_pair(x.x, f);
       x.y = scale_pair(x.y, f);
@@ -797,11 +760,6 @@ int band_of(int64_t mtiles, int64_t contraction) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(mtiles, (48ll << 20) / (TM * contraction * 2))));
 }
 
-// Rows of the A box.  A box reaching past the last token is filled with zeros
-// at a cost: with one token and a full box the logits product of a 32000 x 4096
-// head took 85 us, with 64 tokens 56 us.
-int a_box(int64_t rows) { return rows < UM ? static_cast<int>((rows + 7) / 8 * 8) : UM; }
-
 // Tiles of the logits product.  Their width is the one whose rounds over the
 // resident pairs cost least, 256 if nothing is clearly better.  A stage of a
 // tile costs the bytes a CTA brings from L2 for it (128 token rows and bn / 2 of
@@ -842,7 +800,6 @@ HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
   g.band = band_of(g.mtiles, K);
-  g.abox = a_box(rows);
   return g;
 }
 
@@ -860,7 +817,6 @@ HeadGrid grad_tiles(int64_t rows, int64_t N, int64_t K, int nh, double* cost) {
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
   g.band = g.mtiles;
-  g.abox = a_box(rows);
   const int64_t numK = (N + BK - 1) / BK;
   const int P = head_pairs();
   *cost = 0.0;
@@ -897,6 +853,28 @@ HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
   return two < one ? b : a;
 }
 
+// The column segments of a piece's statistics: the first of a tile's two has sw
+// columns, a tile tn.
+struct Segments {
+  int tn, sw, count;
+};
+Segments segments(int64_t rows, int64_t N, int64_t K) {
+  if (rows <= kHeadFewTokens) {
+    const int br = few_tile_rows(N);
+    return {2 * br, br, static_cast<int>((N + br - 1) / br)};
+  }
+  const HeadGrid g = logits_grid(rows, N, K);
+  return {g.tn, g.sw, 2 * g.ntiles};
+}
+
+// Bytes of the gradient's fp32 sums of split tiles.
+size_t split_bytes(int64_t rows, int64_t N, int64_t K) {
+  if (rows <= 0) return 0;
+  if (rows <= kHeadFewTokens) return static_cast<size_t>(few_splits(N, K)) * rows * K * 4;
+  const HeadGrid d = grad_grid(rows, N, K);
+  return static_cast<size_t>(d.ntail) * d.nsplit * d.tn * TM * 4;
+}
+
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Workspace of a call of M tokens whose pieces hold `rows` (the last one M % rows).
@@ -920,22 +898,23 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
     at += up256(n);
     return q;
   };
-  const HeadGrid g = logits_grid(rows, N, K);
-  if (nf4) s.w16 = static_cast<uint16_t*>(take(static_cast<size_t>(N) * K * 2));
-  s.part = static_cast<float2*>(take(static_cast<size_t>(2 * g.ntiles) * rows * 8));
+  // The last piece's tiles may be narrower (few tokens), and then more.
+  const int64_t last = M % rows;
+  const size_t segs = static_cast<size_t>(rows) * segments(rows, N, K).count,
+               last_segs = last ? static_cast<size_t>(last) * segments(last, N, K).count : 0;
+  if (nf4 && rows > kHeadFewTokens) s.w16 = static_cast<uint16_t*>(take(static_cast<size_t>(N) * K * 2));
+  s.part = static_cast<float2*>(take(std::max(segs, last_segs) * 8));
   s.ztgt = static_cast<float2*>(take(static_cast<size_t>(rows) * k * 8));
   if (distill) {
     s.sidx = static_cast<int*>(take(static_cast<size_t>(rows) * k * 4));
     s.logq = static_cast<float*>(take(static_cast<size_t>(rows) * k * 4));
-    s.off = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * (2 * g.ntiles + 1) * 2));
+    s.off = static_cast<uint16_t*>(take((std::max(segs, last_segs) + rows) * 2));
   }
   if (grad) {
     s.stat = static_cast<RowStat*>(take(static_cast<size_t>(rows) * sizeof(RowStat)));
     s.rscale = static_cast<float2*>(take(static_cast<size_t>(rows) * 8));
     s.e = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * e_pitch(N) * 2));
-    const HeadGrid d = grad_grid(rows, N, K), last = grad_grid(M % rows, N, K);
-    const int64_t sums = std::max(int64_t(d.ntail) * d.nsplit * d.tn, int64_t(last.ntail) * last.nsplit * last.tn);
-    s.split = static_cast<float*>(take(static_cast<size_t>(sums) * TM * 4));
+    s.split = static_cast<float*>(take(std::max(split_bytes(rows, N, K), split_bytes(last, N, K))));
   }
   s.bytes = at;
   return s;
@@ -987,21 +966,27 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
   const auto BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto SW = CU_TENSOR_MAP_SWIZZLE_128B;
   cudaError_t err = cudaSuccess;
-  const uint16_t* W = a.W;
-  if (nf4) {
+  // An NF4 head is expanded once for the pieces of many tokens (its bf16 values
+  // are then read by several tiles); few tokens expand it as they go.  The last
+  // piece may be of the other kind.
+  HeadWeight h{a.W, a.codes, a.absmax_q, a.dq_scale, a.block, a.dq_block, a.N, a.K};
+  if (nf4 && a.piece > kHeadFewTokens) {
     err = launch_dequantize(a.codes, a.absmax_q, a.dq_scale, a.N * a.K, a.block, a.dq_block, s.w16, st);
     if (err != cudaSuccess) return err;
-    W = s.w16;
+    h.W = s.w16;
   }
+  const uint16_t* W = h.W;
   const int64_t lde = e_pitch(a.N);
   for (int64_t r0 = 0; r0 < a.M; r0 += a.piece) {
     const int64_t rows = std::min(a.piece, a.M - r0);
+    const bool few = rows <= kHeadFewTokens;
     const HeadGrid g = logits_grid(rows, a.N, a.K);
+    const Segments seg = segments(rows, a.N, a.K);
     const uint16_t* X = a.X + r0 * a.K;
     CUtensorMap ma, mb, me{};  // me: e as the logits product writes it
-    if (!make_map(&ma, BF16, X, a.K, rows, a.K * 2, BK, g.abox, SW) ||
-        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, BK, g.bn / 2, SW) ||
-        (grad && !make_map(&me, BF16, s.e, lde, rows, lde * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)))
+    if (!few && (!make_map(&ma, BF16, X, a.K, rows, a.K * 2, BK, UM, SW) ||
+                 !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, BK, g.bn / 2, SW) ||
+                 (grad && !make_map(&me, BF16, s.e, lde, rows, lde * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))))
       return cudaErrorInvalidValue;
     HeadEpi p{};
     p.rows = static_cast<int>(rows);
@@ -1021,40 +1006,47 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
       const float inv_t = 1.0f / a.temperature;
       if (a.teacher_bf16)
         err = launch_ex(k_head_targets<__nv_bfloat16>, grid, block, 0, st, true, idx,
-                        static_cast<const __nv_bfloat16*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.tn,
-                        g.sw, 2 * g.ntiles, s.sidx, s.logq, s.off);
+                        static_cast<const __nv_bfloat16*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, seg.tn,
+                        seg.sw, seg.count, s.sidx, s.logq, s.off);
       else
         err = launch_ex(k_head_targets<float>, grid, block, 0, st, true, idx,
-                        static_cast<const float*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, g.tn, g.sw,
-                        2 * g.ntiles, s.sidx, s.logq, s.off);
+                        static_cast<const float*>(a.teacher_logits) + r0 * a.k, a.k, p.cols, inv_t, seg.tn,
+                        seg.sw, seg.count, s.sidx, s.logq, s.off);
       if (err != cudaSuccess) return err;
     }
-    err = g.nh == 2 ? launch_pairs<0, 2>(ma, mb, me, a.K, g, p, st) : launch_pairs<0, 1>(ma, mb, me, a.K, g, p, st);
+    if (few) err = launch_few_logits(h, X, seg.sw, p, st);
+    else if (g.nh == 2) err = launch_pairs<0, 2>(ma, mb, me, a.K, g, p, st);
+    else err = launch_pairs<0, 1>(ma, mb, me, a.K, g, p, st);
     if (err != cudaSuccess) return err;
     err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
                     true,
-                    static_cast<const float2*>(s.part), 2 * g.ntiles, p.rows, p.cols, p.labels,
+                    static_cast<const float2*>(s.part), seg.count, p.rows, p.cols, p.labels,
                     static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
                     static_cast<const float2*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
                     a.lse + r0, s.stat, s.rscale, s.e, lde);
     if (err != cudaSuccess) return err;
     if (!grad) continue;
     err = launch_ex(k_head_rescale, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 4 * device_sm_count()))),
-                    dim3(256), 0, st, true, s.e, lde, static_cast<const float2*>(s.part), g.tn, g.sw, 2 * g.ntiles,
+                    dim3(256), 0, st, true, s.e, lde, static_cast<const float2*>(s.part), seg.tn, seg.sw, seg.count,
                     p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float2*>(s.rscale), p.labels,
                     static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
                     static_cast<const float2*>(s.ztgt));
     if (err != cudaSuccess) return err;
-    const HeadGrid d = grad_grid(rows, a.N, a.K);
-    if (!make_map(&ma, BF16, s.e, lde, rows, lde * 2, BK, d.abox, SW) ||
-        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, 64, BK, SW))
-      return cudaErrorInvalidValue;
     HeadEpi q{};
     q.rows = p.rows;
     q.cols = static_cast<int>(a.K);
     q.rscale = s.rscale;
     q.out = a.dX + r0 * a.K;
     q.split = s.split;
+    if (few) {
+      err = launch_few_grad(h, s.e, lde, few_splits(a.N, a.K), q, st);
+      if (err != cudaSuccess) return err;
+      continue;
+    }
+    const HeadGrid d = grad_grid(rows, a.N, a.K);
+    if (!make_map(&ma, BF16, s.e, lde, rows, lde * 2, BK, UM, SW) ||
+        !make_map(&mb, BF16, W, a.K, a.N, a.K * 2, 64, BK, SW))
+      return cudaErrorInvalidValue;
     err = d.nh == 2 ? launch_pairs<1, 2>(ma, mb, me, a.N, d, q, st) : launch_pairs<1, 1>(ma, mb, me, a.N, d, q, st);
     if (err == cudaSuccess && d.ntail)
       err = launch_ex(k_head_join, dim3(static_cast<unsigned>(d.ntail * (TM * (d.tn / 8) / 256))), dim3(256), 0, st,

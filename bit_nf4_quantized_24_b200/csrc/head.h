@@ -1,0 +1,58 @@
+// What the two translation units of the head losses share: head.cu (the call, and
+// the products for many tokens) and head_few.cu (those for at most 128).
+#pragma once
+
+#include "internal.h"
+
+namespace qn {
+
+constexpr float kHeadFits = 64.0f;  // |reference| (log2) up to which e is stored without it
+constexpr int kHeadFewTokens = 128;
+
+// The frozen head: W, or (W null) the NF4 weight.
+struct HeadWeight {
+  const uint16_t* W;
+  const uint8_t* codes;
+  const uint8_t* absmax_q;
+  const float* dq_scale;
+  int block, dq_block;
+  int64_t N, K;
+};
+
+// What the products' epilogues read and write (MODE 0: logits, MODE 1: gradient).
+struct HeadEpi {
+  int rows;         // token rows of the piece
+  int cols;         // MODE 0: N; MODE 1: K
+  // MODE 0
+  float c;                   // log2(e) / T
+  float2* part;              // [segments][rows], per column segment: (reference n, sum of exp2(z c - n))
+  uint16_t* e;               // [rows][lde] (nullable)
+  int64_t lde;
+  const int64_t* labels;     // [rows] (cross entropy), or
+  const int* sidx;           // [rows][k] targets in ascending order, and
+  const uint16_t* off;       // [rows][segments + 1] first target of each column segment
+  int k;
+  float2* ztgt;              // [rows][k] target logits: (z c - n, n)
+  // MODE 1
+  const float2* rscale;      // [rows] factors (x, y) of the row (y = 0: the row is written as zeros)
+  uint16_t* out;             // [rows][cols]
+  float* split;              // fp32 sums of the split tiles' pieces
+};
+
+// exp2 on the special-function unit: relative error about 2^-22, which is far
+// below the bf16 rounding of e and of the order of the fp32 sums' own rounding.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// At most kHeadFewTokens tokens.  Column segments are tiles of few_tile_rows(N)
+// entries; the gradient's p.split holds few_splits(N, K) x rows x K sums.
+int few_tile_rows(int64_t N);
+int few_splits(int64_t N, int64_t K);
+cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st);
+cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp, int nsplit, const HeadEpi& p,
+                            cudaStream_t st);
+
+}  // namespace qn

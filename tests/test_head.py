@@ -137,6 +137,8 @@ def teacher(g, M, N, k, bf16, empty=True):
 SHAPES = [
     (1, 1, 64), (1, 7, 64), (2, 256, 64), (3, 65, 128), (16, 257, 192), (127, 1000, 64), (128, 255, 512),
     (129, 511, 128), (256, 2048, 256), (257, 513, 64), (300, 2049, 320), (600, 4099, 576), (1, 32003, 1024),
+    (17, 9001, 2112), (100, 5000, 192), (128, 32003, 640),
+    (2290, 4090, 8192),  # tiles of 512 in both products
 ]
 
 
@@ -157,9 +159,9 @@ def test_xent(L, M, N, K, grad):
 
 
 @gpu
-@pytest.mark.parametrize("block,dq", [(32, 0), (32, 256), (64, 256), (128, 0), (256, 256)])
-def test_xent_nf4_head(L, block, dq):
-    M, N, K = 200, 1031, 512
+@pytest.mark.parametrize("M,N,K", [(1, 300, 256), (37, 9001, 512), (128, 1031, 768), (200, 1031, 512)])
+@pytest.mark.parametrize("block,dq", [(32, 0), (32, 256), (64, 256), (64, 0), (128, 0), (256, 256)])
+def test_xent_nf4_head(L, block, dq, M, N, K):
     head, values, X, labels, g = make(block + dq, M, N, K, block, dq)
     dloss = torch.full((M,), 1.0 / M, device="cuda")
     ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)
@@ -303,7 +305,7 @@ def test_pieces_of_tokens(L, piece):
     dloss = torch.rand(M, generator=g).cuda()
     ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)
     compare(qb.qlora_head_xent(head, X, labels, dloss=dloss), ref)
-    nbytes = qb.head_workspace_bytes(M, N, K, piece=piece)
+    nbytes = qb.head_workspace_bytes(M, N, K, piece=piece)  # M = 900: a last piece of 132, and of few tokens below
     assert nbytes < qb.head_workspace_bytes(M, N, K)
     ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     outs = (torch.full((M,), 7.0, device="cuda"), torch.full((M,), 7.0, device="cuda"),
@@ -314,9 +316,13 @@ def test_pieces_of_tokens(L, piece):
     again = qb.qlora_head_xent(head, X, labels, dloss=dloss, workspace=ws)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
     idx, t = teacher(g, M, N, 9, False)
-    ws = torch.empty(qb.head_workspace_bytes(M, N, K, 9, piece=piece), dtype=torch.uint8, device="cuda")
-    got = qb.qlora_head_distill(head, X, idx, t, 2.0, dloss=dloss, workspace=ws)
-    compare(got, reference(values, X, 2.0, *distill_targets(idx, t, N, 2.0), dloss))
+    for m in (M, 2 * piece + 1, 2 * piece + 128):
+        nbytes = qb.head_workspace_bytes(m, N, K, 9, piece=piece)
+        ws = torch.full((nbytes + 4096,), 171, dtype=torch.uint8, device="cuda")
+        a = [x[:m].contiguous() if m <= M else torch.cat((x, x))[:m].contiguous() for x in (X, idx, t, dloss)]
+        got = qb.qlora_head_distill(head, a[0], a[1], a[2], 2.0, dloss=a[3], workspace=ws[:nbytes])
+        compare(got, reference(values, a[0], 2.0, *distill_targets(a[1], a[2], N, 2.0), a[3]))
+        assert (ws[nbytes:] == 171).all()
 
 
 @gpu
