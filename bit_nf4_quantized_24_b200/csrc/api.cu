@@ -283,6 +283,7 @@ int run_head(HeadArgs& a, const uint16_t* W, const uint8_t* codes, const uint8_t
   const void* ptrs[] = {W, codes, X, dX};
   for (const void* p : ptrs)
     if (p && !aligned(p, 16)) return QLORA_ERR_SHAPE;
+  if (codes && !aligned(codes, 32)) return QLORA_ERR_SHAPE;  // read by whole 32-byte sectors
   const void* words[] = {a.labels, a.teacher_idx};
   for (const void* p : words)
     if (p && !aligned(p, 8)) return QLORA_ERR_SHAPE;

@@ -190,15 +190,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (lane == 0) {
       const uint32_t bytes = 2 * (UM + NH * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
       const uint32_t full_at_leader = mapa_shared(full(0), 0);
-      bool ok = true;
-      int n = 0;  // stages issued
+      bool ok = true, issued = false;
+      RingPos r;
       for (int i = first; i < nitems && ok; i += step) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
         const int m0 = mt * TM + static_cast<int>(rank) * UM, n0 = nt * g.tn + static_cast<int>(rank) * bnl;
         for (int k = kbeg; k < kend; ++k) {
-          const int s = n % STAGES;
-          if (!(ok = wait_bounded(empty(s), ((n / STAGES) & 1) ^ 1, abort, status))) break;
+          const int s = r.slot;
+          if (!(ok = wait_bounded(empty(s), r.phase ^ 1, abort, status))) break;
+          issued = true;
           if (leader) mbar_arrive_expect_tx(full(s), bytes);
           const uint32_t bar = full_at_leader + 8u * s, a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
           tma_load_2d_pair(a_s, &tm_a, bar, k * BK, m0);
@@ -211,13 +212,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               tma_load_2d_pair(b_s + h * B_BYTES + 8192, &tm_b, bar, n0 + h * TN + 64, k * BK);
             }
           }
-          ++n;
+          r.advance(1, STAGES);
         }
       }
       // Let the copies already issued land before the CTA exits.  They report to
       // the leader, which cannot see the end of a stage that only one CTA has
       // issued, so each CTA gives its own the time they can need at most.
-      if (!ok && n > 0) {
+      if (!ok && issued) {
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 20000000ull) {
         }
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (leader && lane == 0) {
       const uint32_t idesc = idesc_bf16(TM, g.bn, false, MODE == 1);
       bool ok = true, committed = false;
-      int n = 0, t = 0;  // stages and tiles so far
+      RingPos r;
+      int t = 0;  // tiles so far
       for (int i = first; i < nitems && ok; i += step, ++t) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
@@ -241,10 +243,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = NH == 1 ? tmem + 256u * (t & 1) : tmem;
-        for (int k = kbeg; k < kend; ++k, ++n) {
-          const int s = n % STAGES;
-          const uint32_t ph = (n / STAGES) & 1;
-          if (!(ok = wait_bounded_cluster(full(s), ph, abort, status))) break;
+        for (int k = kbeg; k < kend; ++k, r.advance(1, STAGES)) {
+          const int s = r.slot;
+          if (!(ok = wait_bounded_cluster(full(s), r.phase, abort, status))) break;
           tc_fence_after();
           const uint32_t a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
 #pragma unroll

@@ -47,6 +47,37 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// True in one lane of a converged warp.  The single-thread roles (TMA, MMA) run
+// with the whole warp and issue from the elected lane: their addresses and
+// descriptors are then the same in all lanes, as those instructions want them.
+// In code that only one lane runs, a stage's MMAs took 800 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// wait_bounded by a whole warp: true if all lanes saw the phase complete.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, status));
+}
+__device__ __forceinline__ bool wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, abort, status));
+}
+
+// A position in a ring of stages.  Kept as slot and phase: dividing a running
+// count by the ring's length took longer than the MMAs of a narrow stage.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance(int by, int stages) {  // by may exceed the ring's length
+    slot += by;
+    while (slot >= stages) {
+      slot -= stages;
+      phase ^= 1u;
+    }
+  }
+};
+
 // At most kHeadFewTokens tokens.  Column segments are tiles of few_tile_rows(N)
 // entries; the gradient's p.split holds few_splits(N, K) x rows x K sums.
 int few_tile_rows(int64_t N);

@@ -19,12 +19,11 @@ namespace qn {
 namespace {
 
 constexpr int UM = 128;              // MMA rows: vocabulary entries (MODE 0) or hidden columns (MODE 1)
-constexpr int BK = 64;
-constexpr int W_BYTES = UM * BK * 2;  // expanded head tile of a stage
-constexpr int C_BYTES = UM * BK / 2;  // its NF4 codes
-constexpr int MAX_STAGES = 12;
-constexpr int CSTAGES = 12;           // NF4 code ring
-constexpr int DQ_GROUPS = 4;          // groups of 4 warps, each expanding every fourth stage
+constexpr int BK = 64;                // contraction of a sub-stage (a 128-byte row of each operand)
+constexpr int SUB = 2;                // sub-stages per stage: waits and commits are paid per stage
+constexpr int W_BYTES = UM * BK * 2;  // head tile of a sub-stage, in bf16
+constexpr int MAX_STAGES = 6;
+constexpr int DQ_GROUPS = 4;          // groups of 4 warps that take turns at expanding the stages
 constexpr int BUF_PITCH = UM + 4;     // floats per token in the epilogue's buffer
 constexpr int BUF_TOKENS = 16;
 constexpr int BUF_BYTES = 2 * BUF_TOKENS * BUF_PITCH * 4;
@@ -34,8 +33,6 @@ constexpr int SMEM_MAX = 232448;
 struct FewBars {
   uint64_t full[MAX_STAGES];   // head tile and token tile landed (or were written)
   uint64_t empty[MAX_STAGES];  // MMAs of the stage completed
-  uint64_t full_c[CSTAGES];    // NF4: code tile landed
-  uint64_t empty_c[CSTAGES];   // NF4: code tile expanded
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -47,7 +44,7 @@ struct FewGrid {
   int tiles;   // tiles along the MMA rows
   int br;      // MMA rows of a tile (MODE 0: vocabulary entries, a multiple of 8 up to 128; MODE 1: 128)
   int nsplit;  // pieces of the contraction (MODE 1)
-  int numK;    // stages of the contraction
+  int numK;    // stages of the contraction (SUB x 64 each)
   int tp;      // tokens, rounded up to 16
   int stages;
   int cols;    // TMEM columns
@@ -87,25 +84,22 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 template <int MODE, int KIND>
 __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
     k_few(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, FewGrid g, HeadEpi p,
-          const uint8_t* __restrict__ absmax_q, const float* __restrict__ dq_scale, Nf4Levels lv, int N, int K, int lg,
+          const uint8_t* __restrict__ codes, const uint8_t* __restrict__ absmax_q, const float* __restrict__ dq_scale, Nf4Levels lv, int N, int K, int lg,
           int dq, int* status) {
   constexpr bool NF4 = KIND > 0, GEN = KIND == 2;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  const int stage_bytes = W_BYTES + g.tp * BK * 2;
-  const uint32_t codes = base + g.stages * stage_bytes;
-  const uint32_t buf = codes + (NF4 ? CSTAGES * C_BYTES : 0);
+  const int x_tile = g.tp * BK * 2, stage_bytes = SUB * (W_BYTES + x_tile);
+  const uint32_t buf = base + g.stages * stage_bytes;
   const uint32_t bar0 = buf + BUF_BYTES;
   FewBars* bars = reinterpret_cast<FewBars*>(smem_raw + (bar0 - raw));
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
-  auto full_c = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + s); };
-  auto empty_c = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + CSTAGES + s); };
-  auto acc_full = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + 2 * CSTAGES + a); };
-  auto acc_empty = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + 2 * CSTAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 2 * CSTAGES + 4);
+  auto acc_full = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + a); };
+  auto acc_empty = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 4);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nitems = g.tiles * g.nsplit, tokens = p.rows;
@@ -124,10 +118,6 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       mbar_init(full(s), NF4 ? 1 + 4 : 1);  // the producer, and the four warps that expand the stage
       mbar_init(empty(s), 1);
     }
-    for (int s = 0; s < CSTAGES; ++s) {
-      mbar_init(full_c(s), 1);
-      mbar_init(empty_c(s), 4);
-    }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full(a), 1);
       mbar_init(acc_empty(a), 4);
@@ -137,14 +127,15 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_w);
+    if (!NF4) tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
   }
   if (tokens < g.tp) {  // the token rows that no copy writes hold zeros
     const int n = (g.tp - tokens) * BK * 2 / 16;
-    for (int s = 0; s < g.stages; ++s)
+    for (int s = 0; s < g.stages * SUB; ++s)
       for (int i = threadIdx.x; i < n; i += blockDim.x)
-        st_shared_v4(base + s * stage_bytes + W_BYTES + tokens * BK * 2 + 16 * i, 0u, 0u, 0u, 0u);
+        st_shared_v4(base + s / SUB * stage_bytes + SUB * W_BYTES + s % SUB * x_tile + tokens * BK * 2 + 16 * i, 0u, 0u,
+                     0u, 0u);
     fence_proxy_async_smem();
   }
   if (warp == 1) {
@@ -159,103 +150,76 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint32_t x_bytes = tokens * BK * 2, w_bytes = MODE == 0 ? g.br * BK * 2 : W_BYTES;
-      bool ok = true;
-      int n = 0;
-      if (!NF4) {
-        for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
-          int nt, z, kbeg, kend;
-          item(i, nt, z, kbeg, kend);
-          for (int k = kbeg; k < kend; ++k, ++n) {
-            const int s = n % g.stages;
-            if (!(ok = wait_bounded(empty(s), ((n / g.stages) & 1) ^ 1, abort, status))) break;
-            const uint32_t w_s = base + s * stage_bytes;
-            mbar_arrive_expect_tx(full(s), w_bytes + x_bytes);
-            if (MODE == 0) {
-              tma_load_2d(w_s, &tm_w, full(s), k * BK, nt * g.br);
-            } else {
-              tma_load_2d(w_s, &tm_w, full(s), nt * UM, k * BK);
-              tma_load_2d(w_s + 8192, &tm_w, full(s), nt * UM + 64, k * BK);
+    const uint32_t x_bytes = tokens * BK * 2, w_bytes = NF4 ? 0 : MODE == 0 ? g.br * BK * 2 : W_BYTES;
+    bool ok = true, issued = false;
+    RingPos r;
+    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x) {
+      int nt, z, kbeg, kend;
+      item(i, nt, z, kbeg, kend);
+      for (int k = kbeg; k < kend; ++k, r.advance(1, g.stages)) {
+        if (!(ok = wait_warp(empty(r.slot), r.phase ^ 1, abort, status))) break;
+        issued = true;
+        if (elect_one()) {
+          const uint32_t bar = full(r.slot), w_s = base + r.slot * stage_bytes;
+          mbar_arrive_expect_tx(bar, SUB * (w_bytes + x_bytes));
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {  // past the end of the contraction: zeros
+            const int at = (k * SUB + u) * BK;
+            if (!NF4 && MODE == 0) {
+              tma_load_2d(w_s + u * W_BYTES, &tm_w, bar, at, nt * g.br);
+            } else if (!NF4) {
+              tma_load_2d(w_s + u * W_BYTES, &tm_w, bar, nt * UM, at);
+              tma_load_2d(w_s + u * W_BYTES + 8192, &tm_w, bar, nt * UM + 64, at);
             }
-            tma_load_2d(w_s + W_BYTES, &tm_x, full(s), k * BK, 0);
+            tma_load_2d(w_s + SUB * W_BYTES + u * x_tile, &tm_x, bar, at, 0);
           }
         }
-      } else {
-        // Two walks over the same stages: the codes run ahead as far as their ring
-        // allows, the token tiles follow the expanded stages.
-        struct Walk {
-          int i, nt, z, k, kend, n;
-        };
-        auto start = [&](Walk& w) {
-          if (w.i < nitems) item(w.i, w.nt, w.z, w.k, w.kend);
-        };
-        auto advance = [&](Walk& w) {
-          ++w.n;
-          if (++w.k == w.kend) {
-            w.i += gridDim.x;
-            start(w);
-          }
-        };
-        Walk c{static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0}, x = c;
-        start(c);
-        start(x);
-        while (x.i < nitems && ok) {
-          while (c.i < nitems && c.n < x.n + CSTAGES - 1 && ok) {
-            const int s = c.n % CSTAGES;
-            if (!(ok = wait_bounded(empty_c(s), ((c.n / CSTAGES) & 1) ^ 1, abort, status))) break;
-            mbar_arrive_expect_tx(full_c(s), MODE == 0 ? g.br * (BK / 2) : C_BYTES);
-            if (MODE == 0) tma_load_2d(codes + s * C_BYTES, &tm_w, full_c(s), c.k * (BK / 2), c.nt * g.br);
-            else tma_load_2d(codes + s * C_BYTES, &tm_w, full_c(s), c.nt * (UM / 2), c.k * BK);
-            advance(c);
-          }
-          if (!ok) break;
-          const int s = x.n % g.stages;
-          if (!(ok = wait_bounded(empty(s), ((x.n / g.stages) & 1) ^ 1, abort, status))) break;
-          mbar_arrive_expect_tx(full(s), x_bytes);
-          tma_load_2d(base + s * stage_bytes + W_BYTES, &tm_x, full(s), x.k * BK, 0);
-          advance(x);
-        }
-        n = c.n;
+        __syncwarp();
       }
-      if (!ok && n > 0) {  // the copies already issued land well within this time
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 20000000ull) {
-        }
+    }
+    if (!ok && issued) {  // the copies already issued land well within this time
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 20000000ull) {
       }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(UM, g.tp, MODE == 1, false);
-      bool ok = true, committed = false;
-      int n = 0, t = 0;
-      for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++t) {
-        int nt, z, kbeg, kend;
-        item(i, nt, z, kbeg, kend);
-        if (!(ok = wait_bounded(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
+    const uint32_t idesc = idesc_bf16(UM, g.tp, MODE == 1, false);
+    bool ok = true, committed = false;
+    RingPos r;
+    int t = 0;
+    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++t) {
+      int nt, z, kbeg, kend;
+      item(i, nt, z, kbeg, kend);
+      if (!(ok = wait_warp(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (t & 1) * g.tp;
+      for (int k = kbeg; k < kend; ++k, r.advance(1, g.stages)) {
+        if (!(ok = wait_warp(full(r.slot), r.phase, abort, status))) break;
         tc_fence_after();
-        const uint32_t d = tmem + (t & 1) * g.tp;
-        for (int k = kbeg; k < kend; ++k, ++n) {
-          const int s = n % g.stages;
-          if (!(ok = wait_bounded(full(s), (n / g.stages) & 1, abort, status))) break;
-          tc_fence_after();
-          const uint32_t w_s = base + s * stage_bytes, x_s = w_s + W_BYTES;
+        const uint32_t w_s = base + r.slot * stage_bytes, x_s = w_s + SUB * W_BYTES;
+        const uint64_t ad = MODE == 0 ? desc_sw128(w_s, 16, 1024) : desc_sw128(w_s, 8192, 1024);
+        const uint64_t bd = desc_sw128(x_s, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = MODE == 0 ? desc_sw128(w_s + kk * 32, 16, 1024) : desc_sw128(w_s + kk * 2048, 8192, 1024);
-            tc_mma_f16(d, ad, desc_sw128(x_s + kk * 32, 16, 1024), idesc, (k > kbeg || kk > 0) ? 1u : 0u);
-          }
-          tc_commit(empty(s));
-          committed = true;
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)  // a descriptor's low bits are the address / 16
+              tc_mma_f16(d, ad + u * (W_BYTES / 16) + kk * (MODE == 0 ? 2 : 128), bd + u * (x_tile / 16) + kk * 2, idesc,
+                         (k > kbeg || u + kk > 0) ? 1u : 0u);
+          tc_commit(empty(r.slot));
         }
-        if (ok) tc_commit(acc_full(t & 1));
+        __syncwarp();
+        committed = true;
       }
-      if (!ok && committed) {
-        tc_commit(drain_bar);
-        wait_drain(drain_bar, 0);
-      }
+      if (ok && elect_one()) tc_commit(acc_full(t & 1));
+      __syncwarp();
     }
+    if (!ok && committed && elect_one()) {
+      tc_commit(drain_bar);
+      wait_drain(drain_bar, 0);
+    }
+    __syncwarp();
   } else if (warp < 6) {
     // ------------------------------------------------------------- epilogue
     const int quad = warp & 3, ew = warp - 2;
@@ -298,29 +262,46 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
 #pragma unroll
           for (int j = 0; j < BUF_TOKENS; ++j) bp[j * BUF_PITCH + quad * 32 + lane] = __uint_as_float(v[j]);
           epilogue_barrier();
-          for (int j = ew * (BUF_TOKENS / 4); j < (ew + 1) * (BUF_TOKENS / 4) && m + j < tokens; ++j) {
-            const int row = m + j, c0 = 4 * lane;
-            const float4 x4 = *reinterpret_cast<const float4*>(bp + j * BUF_PITCH + c0);
-            const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-            float mx = -INFINITY;
+          // The warp's four tokens together: each step is a chain of shuffles.
+          constexpr int TW = BUF_TOKENS / 4;
+          const int j0 = ew * TW, c0 = 4 * lane;
+          float e[TW][4], ref[TW], sum[TW], mx[TW];
+#pragma unroll
+          for (int u = 0; u < TW; ++u) {
+            const float4 x = *reinterpret_cast<const float4*>(bp + (j0 + u) * BUF_PITCH + c0);
+            e[u][0] = x.x, e[u][1] = x.y, e[u][2] = x.z, e[u][3] = x.w;
+            mx[u] = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (c0 + q < ncols) mx = fmaxf(mx, x[q]);
-            for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float ref = mx == -INFINITY ? 0.0f : rintf(mx * p.c);  // as in head.cu
-            float e[4], sum;
+              if (c0 + q < ncols) mx[u] = fmaxf(mx[u], e[u][q]);
+          }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e[q] = c0 + q < ncols ? exp2_fast(fmaf(x[q], p.c, -ref)) : 0.0f;
-            sum = (e[0] + e[1]) + (e[2] + e[3]);
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+            for (int u = 0; u < TW; ++u) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], d));
+#pragma unroll
+          for (int u = 0; u < TW; ++u) {
+            ref[u] = mx[u] == -INFINITY ? 0.0f : rintf(mx[u] * p.c);  // as in head.cu
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e[u][q] = c0 + q < ncols ? exp2_fast(fmaf(e[u][q], p.c, -ref[u])) : 0.0f;
+            sum[u] = (e[u][0] + e[u][1]) + (e[u][2] + e[u][3]);
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+            for (int u = 0; u < TW; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
+#pragma unroll
+          for (int u = 0; u < TW; ++u) {
+            const int j = j0 + u, row = m + j;
+            if (row >= tokens) break;
             if (lane == 0)
-              p.part[static_cast<int64_t>(nt) * tokens + row] = make_float2(mx == -INFINITY ? mx : ref, sum);
+              p.part[static_cast<int64_t>(nt) * tokens + row] = make_float2(mx[u] == -INFINITY ? mx[u] : ref[u], sum[u]);
             if (p.e) {
               uint16_t* er = p.e + static_cast<int64_t>(row) * p.lde + v0;
-              const float back = exp2f(fabsf(ref) <= kHeadFits ? ref : 0.0f);
+              const float back = exp2f(fabsf(ref[u]) <= kHeadFits ? ref[u] : 0.0f);
               if (c0 < ewidth)  // groups of four entries are whole: br % 8 == 0, lde % 64 == 0
-                *reinterpret_cast<uint2*>(er + c0) =
-                    make_uint2(bf16x2_bits(e[0] * back, e[1] * back), bf16x2_bits(e[2] * back, e[3] * back));
+                *reinterpret_cast<uint2*>(er + c0) = make_uint2(bf16x2_bits(e[u][0] * back, e[u][1] * back),
+                                                                bf16x2_bits(e[u][2] * back, e[u][3] * back));
               if (nt == g.tiles - 1)  // the pitch may reach past the last tile
                 for (int64_t c = v0 + g.br + c0; c < p.lde; c += 128)
                   *reinterpret_cast<uint2*>(er + (c - v0)) = make_uint2(0u, 0u);
@@ -328,12 +309,12 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
             if (p.labels) {
               const int64_t y = p.labels[row];
               if (lane == 0 && y >= v0 && y < v0 + ncols)
-                p.ztgt[row] = make_float2(fmaf(bp[j * BUF_PITCH + static_cast<int>(y - v0)], p.c, -ref), ref);
+                p.ztgt[row] = make_float2(fmaf(bp[j * BUF_PITCH + static_cast<int>(y - v0)], p.c, -ref[u]), ref[u]);
             } else {
               const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.tiles + 1) + nt;
               for (int s = o[0] + lane; s < o[1]; s += 32) {
                 const int64_t at = static_cast<int64_t>(row) * p.k + s;
-                p.ztgt[at] = make_float2(fmaf(bp[j * BUF_PITCH + p.sidx[at] - v0], p.c, -ref), ref);
+                p.ztgt[at] = make_float2(fmaf(bp[j * BUF_PITCH + p.sidx[at] - v0], p.c, -ref[u]), ref[u]);
               }
             }
           }
@@ -345,19 +326,23 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
     }
   } else if (NF4) {
     // ----------------------------------------------- expansion of the codes
+    // Never more groups than stages: a group that has expanded stage n knows that
+    // stage n - stages is consumed, and no more; stage n + groups must not lie two
+    // turns of the ring past the last stage known to be consumed, because a phase's
+    // parity cannot tell the two turns apart.
+    const int groups = min(DQ_GROUPS, g.stages);
     const int e = warp - 6, grp = e >> 2;
     const int t = (e & 3) * 32 + lane;  // row of the 128-byte rows of the stage
     const int KB = K / 64;
     // Which (row, 64-weight group) of W this thread expands: MODE 0, row t of the
     // tile; MODE 1, row t % 64 of the stage, columns 64 (t / 64) of the tile.
     struct Walk {
-      int i, nt, z, k, kend, n;
+      int i, nt, z, k, kend;
     };
     auto start = [&](Walk& w) {
       if (w.i < nitems) item(w.i, w.nt, w.z, w.k, w.kend);
     };
     auto advance = [&](Walk& w, int by) {  // by stages; an item may be shorter than that
-      w.n += by;
       w.k += by;
       while (w.i < nitems && w.k >= w.kend) {
         const int over = w.k - w.kend;
@@ -366,86 +351,64 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
         w.k += over;
       }
     };
-    struct Scale {
+    // The codes go from global memory to registers (32 bytes per thread and
+    // sub-stage: a whole sector), one of the group's stages ahead, with the one or
+    // two scales of their blocks.  Each sub-stage has its own registers: handing
+    // them on by moves would wait for the loads.
+    struct Part {
+      uint32_t c[8];
       uint32_t q0, q1;
       float s0, s1;
       bool valid;
     };
-    auto fetch = [&](const Walk& w) {
-      Scale sc{0u, 0u, 0.0f, 0.0f, false};
-      if (w.i >= nitems) return sc;
-      const int wrow = MODE == 0 ? w.nt * g.br + t : w.k * BK + (t & 63);
-      const int kcol = MODE == 0 ? w.k * BK : w.nt * UM + 64 * (t >> 6);
-      if (wrow < N && kcol < K && (MODE == 1 || t < g.br)) {
-        if (!GEN) {
-          const int64_t blk = static_cast<int64_t>(wrow) * KB + (kcol >> 6);
-          sc.q0 = __ldg(absmax_q + blk);
-          sc.s0 = __ldg(dq_scale + (blk >> 8));
-        } else {
-          const int64_t blk = (static_cast<int64_t>(wrow) * K + kcol) >> lg;
-          if (dq) {
-            sc.q0 = __ldg(absmax_q + blk);
-            sc.s0 = __ldg(dq_scale + (blk >> 8));
-            if (lg == 5) {
-              sc.q1 = __ldg(absmax_q + blk + 1);
-              sc.s1 = __ldg(dq_scale + ((blk + 1) >> 8));
-            }
-          } else {
-            sc.s0 = __ldg(dq_scale + blk);
-            if (lg == 5) sc.s1 = __ldg(dq_scale + blk + 1);
+    auto fetch = [&](const Walk& w, int u, Part& f) {
+      f.valid = false;
+      if (w.i >= nitems) return;
+      const int at0 = (w.k * SUB + u) * BK;
+      const int wrow = MODE == 0 ? w.nt * g.br + t : at0 + (t & 63);
+      const int kcol = MODE == 0 ? at0 : w.nt * UM + 64 * (t >> 6);
+      if (wrow >= N || kcol >= K || (MODE == 0 && t >= g.br)) return;
+      f.valid = true;
+      const int64_t at = static_cast<int64_t>(wrow) * K + kcol;
+      ldg_nc_v8(codes + at / 2, f.c);
+      if (!GEN) {
+        f.q0 = __ldg(absmax_q + (at >> 6));
+        f.s0 = __ldg(dq_scale + (at >> 14));
+      } else {
+        const int64_t blk = at >> lg;
+        if (dq) {
+          f.q0 = __ldg(absmax_q + blk);
+          f.s0 = __ldg(dq_scale + (blk >> 8));
+          if (lg == 5) {
+            f.q1 = __ldg(absmax_q + blk + 1);
+            f.s1 = __ldg(dq_scale + ((blk + 1) >> 8));
           }
+        } else {
+          f.s0 = __ldg(dq_scale + blk);
+          if (lg == 5) f.s1 = __ldg(dq_scale + blk + 1);
         }
-        sc.valid = true;
       }
-      return sc;
     };
-    // The scales are loaded two of this group's stages ahead.
-    Walk w{static_cast<int>(blockIdx.x), 0, 0, 0, 0, 0};
-    start(w);
-    advance(w, grp);
-    Walk a1 = w;
-    Scale p0 = fetch(a1);
-    advance(a1, DQ_GROUPS);
-    Scale p1 = fetch(a1);
-    Walk a2 = a1;
-    bool ok = true;
-    while (w.i < nitems && ok) {
-      advance(a2, DQ_GROUPS);
-      const Scale p2 = fetch(a2);
-      const int cs = w.n % CSTAGES, s = w.n % g.stages;
-      if (!(ok = wait_bounded(full_c(cs), (w.n / CSTAGES) & 1, abort, status))) break;
-      const uint32_t c_s = codes + cs * C_BYTES;
-      uint4 q0, q1;
-      if (MODE == 0) {  // code tile [br rows][32 B], 32-byte swizzle
-        const uint32_t sw = (static_cast<uint32_t>(t) >> 2) & 1u;
-        q0 = ld_shared_v4(c_s + t * 32 + ((0u ^ sw) << 4));
-        q1 = ld_shared_v4(c_s + t * 32 + ((1u ^ sw) << 4));
-      } else {  // code tile [64 rows][64 B], 64-byte swizzle
-        const uint32_t row = t & 63, j = t >> 6, sw = (row >> 1) & 3u;
-        q0 = ld_shared_v4(c_s + row * 64 + (((2 * j) ^ sw) << 4));
-        q1 = ld_shared_v4(c_s + row * 64 + (((2 * j + 1) ^ sw) << 4));
-      }
-      if (!(ok = wait_bounded(empty(s), ((w.n / g.stages) & 1) ^ 1, abort, status))) break;
-      const uint32_t row_s = base + s * stage_bytes + t * 128;
+    RingPos r;
+    auto expand = [&](int u, const Part& f) {
+      const uint32_t row_s = base + r.slot * stage_bytes + u * W_BYTES + t * 128;
       const uint32_t sw = t & 7;
-      if (p0.valid) {
-        const float a0 = (GEN && !dq) ? p0.s0 : __fmul_rn(static_cast<float>(p0.q0), p0.s0);
+      if (f.valid) {
+        const float a0 = (GEN && !dq) ? f.s0 : __fmul_rn(static_cast<float>(f.q0), f.s0);
         const Nf4Lut lut = make_lut(lv, a0);
-        const uint32_t c[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
         if (GEN && lg == 5) {
-          const float a1s = dq ? __fmul_rn(static_cast<float>(p0.q1), p0.s1) : p0.s1;
-          const Nf4Lut lut1 = make_lut(lv, a1s);
+          const Nf4Lut lut1 = make_lut(lv, dq ? __fmul_rn(static_cast<float>(f.q1), f.s1) : f.s1);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint32_t o0, o1, o2, o3;
-            deq8(c[j], j < 4 ? lut : lut1, o0, o1, o2, o3);
+            deq8(f.c[j], j < 4 ? lut : lut1, o0, o1, o2, o3);
             st_shared_v4(row_s + ((j ^ sw) << 4), o0, o1, o2, o3);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint32_t o0, o1, o2, o3;
-            deq8(c[j], lut, o0, o1, o2, o3);
+            deq8(f.c[j], lut, o0, o1, o2, o3);
             st_shared_v4(row_s + ((j ^ sw) << 4), o0, o1, o2, o3);
           }
         }
@@ -453,15 +416,26 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) st_shared_v4(row_s + (j << 4), 0u, 0u, 0u, 0u);
       }
+    };
+    static_assert(SUB == 2, "one set of registers per sub-stage");
+    Walk w{grp < groups ? static_cast<int>(blockIdx.x) : nitems, 0, 0, 0, 0};
+    start(w);
+    advance(w, grp);
+    r.advance(grp, g.stages);
+    Part a, b;
+    fetch(w, 0, a);
+    fetch(w, 1, b);
+    while (w.i < nitems) {
+      if (!wait_warp(empty(r.slot), r.phase ^ 1, abort, status)) break;
+      advance(w, groups);
+      expand(0, a);
+      fetch(w, 0, a);
+      expand(1, b);
+      fetch(w, 1, b);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(empty_c(cs));
-        mbar_arrive(full(s));
-      }
-      advance(w, DQ_GROUPS);
-      p0 = p1;
-      p1 = p2;
+      if (lane == 0) mbar_arrive(full(r.slot));
+      r.advance(groups, g.stages);
     }
   }
 
@@ -494,18 +468,18 @@ __global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ spli
 }
 
 // Ring depth and shared memory for `tokens` tokens.
-int few_stages(int tp, bool nf4) {
-  const int room = SMEM_MAX - 1024 - BAR_BYTES - BUF_BYTES - (nf4 ? CSTAGES * C_BYTES : 0);
-  return std::min(MAX_STAGES, room / (W_BYTES + tp * BK * 2));
+int few_stages(int tp) {
+  const int room = SMEM_MAX - 1024 - BAR_BYTES - BUF_BYTES;
+  return std::min(MAX_STAGES, room / (SUB * (W_BYTES + tp * BK * 2)));
 }
-int few_smem(const FewGrid& g, bool nf4) {
-  return 1024 + g.stages * (W_BYTES + g.tp * BK * 2) + (nf4 ? CSTAGES * C_BYTES : 0) + BUF_BYTES + BAR_BYTES;
+int few_smem(const FewGrid& g) {
+  return 1024 + g.stages * SUB * (W_BYTES + g.tp * BK * 2) + BUF_BYTES + BAR_BYTES;
 }
 
-FewGrid few_grid(int64_t tokens, bool nf4) {
+FewGrid few_grid(int64_t tokens) {
   FewGrid g{};
   g.tp = static_cast<int>((tokens + 15) / 16 * 16);
-  g.stages = few_stages(g.tp, nf4);
+  g.stages = few_stages(g.tp);
   g.cols = 32;
   while (g.cols < 2 * g.tp) g.cols *= 2;
   return g;
@@ -519,8 +493,8 @@ cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& x, const FewGri
   int lg = 0;
   while ((1 << lg) < h.block) ++lg;
   const int grid = std::min(g.tiles * g.nsplit, device_sm_count());
-  return launch_ex(k_few<MODE, KIND>, dim3(grid), dim3(KIND ? 192 + DQ_GROUPS * 128 : 192), few_smem(g, KIND > 0), st,
-                   true, w, x, g, p, h.absmax_q, h.dq_scale, host_codebook().levels, static_cast<int>(h.N),
+  return launch_ex(k_few<MODE, KIND>, dim3(grid), dim3(KIND ? 192 + DQ_GROUPS * 128 : 192), few_smem(g), st,
+                   true, w, x, g, p, h.codes, h.absmax_q, h.dq_scale, host_codebook().levels, static_cast<int>(h.N),
                    static_cast<int>(h.K), lg, h.dq_block ? 1 : 0, device_status_ptr());
 }
 template <int MODE>
@@ -532,7 +506,6 @@ cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& x, const FewGrid
 }
 
 const auto BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 const auto SW128 = CU_TENSOR_MAP_SWIZZLE_128B;
 
 }  // namespace
@@ -556,14 +529,14 @@ int few_tile_rows(int64_t N) {
 }
 
 int few_splits(int64_t N, int64_t K) {
-  const int64_t tiles = (K + UM - 1) / UM, numK = (N + BK - 1) / BK;
+  const int64_t tiles = (K + UM - 1) / UM, numK = (N + SUB * BK - 1) / (SUB * BK);
   const int P = device_sm_count();
   int best = 1;
   double cost = 0.0;
-  for (int64_t S = 1; S <= std::min<int64_t>(std::max<int64_t>(numK / 8, 1), 64); ++S) {
+  for (int64_t S = 1; S <= std::min<int64_t>(std::max<int64_t>(numK / 4, 1), 64); ++S) {
     const double rounds = static_cast<double>((tiles * S + P - 1) / P);
-    // rounds of S-ths of the vocabulary, each with its start and epilogue (about 4 stages)
-    const double c = rounds * (static_cast<double>(numK) / static_cast<double>(S) + 4.0);
+    // rounds of S-ths of the vocabulary, each with its start and epilogue (about 2 stages)
+    const double c = rounds * (static_cast<double>(numK) / static_cast<double>(S) + 2.0);
     if (S == 1 || c < cost) {
       cost = c;
       best = static_cast<int>(S);
@@ -573,29 +546,27 @@ int few_splits(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, !h.W);
+  FewGrid g = few_grid(p.rows);
   g.br = br;
   g.tiles = static_cast<int>((h.N + br - 1) / br);
   g.nsplit = 1;
-  g.numK = static_cast<int>(h.K / BK);
-  CUtensorMap w, x;
-  const bool ok = h.W ? make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, BK, br, SW128)
-                      : make_map(&w, U8, h.codes, h.K / 2, h.N, h.K / 2, BK / 2, br, CU_TENSOR_MAP_SWIZZLE_32B);
-  if (!ok || !make_map(&x, BF16, X, h.K, p.rows, h.K * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
+  g.numK = static_cast<int>((h.K + SUB * BK - 1) / (SUB * BK));
+  CUtensorMap w{}, x;
+  if ((h.W && !make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, BK, br, SW128)) ||
+      !make_map(&x, BF16, X, h.K, p.rows, h.K * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
   return launch_few<0>(w, x, g, p, h, st);
 }
 
 cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp, int nsplit, const HeadEpi& p,
                             cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, !h.W);
+  FewGrid g = few_grid(p.rows);
   g.br = UM;
   g.tiles = static_cast<int>((h.K + UM - 1) / UM);
   g.nsplit = nsplit;
-  g.numK = static_cast<int>((h.N + BK - 1) / BK);
-  CUtensorMap w, x;
-  const bool ok = h.W ? make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, 64, BK, SW128)
-                      : make_map(&w, U8, h.codes, h.K / 2, h.N, h.K / 2, UM / 2, BK, CU_TENSOR_MAP_SWIZZLE_64B);
-  if (!ok || !make_map(&x, BF16, P, ldp, p.rows, ldp * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
+  g.numK = static_cast<int>((h.N + SUB * BK - 1) / (SUB * BK));
+  CUtensorMap w{}, x;
+  if ((h.W && !make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, 64, BK, SW128)) ||
+      !make_map(&x, BF16, P, ldp, p.rows, ldp * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
   cudaError_t e = launch_few<1>(w, x, g, p, h, st);
   if (e != cudaSuccess) return e;
   return launch_ex(k_few_join, dim3(static_cast<unsigned>((p.cols + 511) / 512), static_cast<unsigned>(p.rows)),

@@ -334,9 +334,10 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  * which gets none).  The logits are never stored.
  *
  * The head is given EITHER as W, bf16 [N, K], OR (W NULL) as an NF4 weight in
- * any codec format: codes, absmax_q, dq_scale, block, dq_block as above
- * (K % block == 0); an NF4 head is expanded to bf16 once per call, in the
- * workspace.  With a bf16 head the NF4 arguments are ignored (codes NULL).
+ * any codec format: codes (32-byte aligned), absmax_q, dq_scale, block, dq_block
+ * as above (K % block == 0); for more than 128 tokens an NF4 head is expanded to
+ * bf16 once per call, in the workspace, and for fewer as the products read it.
+ * With a bf16 head the NF4 arguments are ignored (codes NULL).
  *
  * qlora_head_xent, softmax cross entropy with z = X W^T:
  *     lse[m]  = log sum_j exp z[m, j]

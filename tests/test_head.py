@@ -137,7 +137,7 @@ def teacher(g, M, N, k, bf16, empty=True):
 SHAPES = [
     (1, 1, 64), (1, 7, 64), (2, 256, 64), (3, 65, 128), (16, 257, 192), (127, 1000, 64), (128, 255, 512),
     (129, 511, 128), (256, 2048, 256), (257, 513, 64), (300, 2049, 320), (600, 4099, 576), (1, 32003, 1024),
-    (17, 9001, 2112), (100, 5000, 192), (128, 32003, 640),
+    (17, 9001, 2112), (100, 5000, 192), (128, 32003, 640), (40, 40001, 64), (90, 33333, 128),
     (2290, 4090, 8192),  # tiles of 512 in both products
 ]
 
@@ -159,7 +159,8 @@ def test_xent(L, M, N, K, grad):
 
 
 @gpu
-@pytest.mark.parametrize("M,N,K", [(1, 300, 256), (37, 9001, 512), (128, 1031, 768), (200, 1031, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 256), (37, 9001, 512), (128, 1031, 768), (200, 1031, 512),
+                                   (100, 32000, 2048), (128, 20001, 1280), (16, 32000, 1024)])
 @pytest.mark.parametrize("block,dq", [(32, 0), (32, 256), (64, 256), (64, 0), (128, 0), (256, 256)])
 def test_xent_nf4_head(L, block, dq, M, N, K):
     head, values, X, labels, g = make(block + dq, M, N, K, block, dq)
@@ -526,6 +527,7 @@ def test_refusals(L):
     assert xent(W=None, codes=f, dq=f) == -1  # double quantization without absmax_q
     assert xent(W=None, codes=f, absmax=f, dq=f, block=48) == -7
     assert xent(W=None, codes=f, absmax=f, dq=f, block=128) == -2
+    assert xent(W=None, codes=P(0x10010), absmax=f, dq=f) == -2  # codes are read by 32 bytes
     assert xent(K=100) == -2 and xent(N=0) == -1 and xent(M=-1) == -1 and xent(M=(1 << 24) + 1) == -2
     assert xent(X=None) == -1 and xent(labels=None) == -1 and xent(loss=None) == -1 and xent(lse=None) == -1
     assert xent(dX=None) == -1  # a gradient's weights without a gradient
