@@ -15,9 +15,12 @@
 // lse and loss.  For the gradient the same kernel also writes e = exp(z) in bf16
 // for a piece of the tokens, and k_head<1> multiplies e by W once lse is known:
 // p = e exp(-lse) is a factor of the whole row, so it waits for the epilogue,
-// and only the target columns of e change in between (they hold p - q, computed
-// from their fp32 logits: p - 1 from a rounded p would be noise for a confident
-// token).  So a loss with its gradient costs two products and no pass over the
+// and only the target columns of e change in between, because p - q from a rounded
+// p would be noise for a confident token: the teacher's hold p - q, computed from
+// their fp32 logits and rounded once; the label's holds 0, and its p - 1 times its
+// row of W is added in fp32 (it is most of the gradient, and p - 1 is -1 for most
+// tokens: rounded after the row's factor it alone made the error of dX 1.5 times
+// that of a bf16 result).  So a loss with its gradient costs two products and no pass over the
 // exponentials.
 //  - Computing p from the logits a second time would need three products.
 //  - Keeping the logits themselves in bf16 would cost accuracy: a rounding error
@@ -46,6 +49,7 @@ constexpr int B_BYTES = TN / 2 * BK * 2;  // per accumulator
 constexpr int RING_BYTES = 192 * 1024;    // 6 stages of 32 KB (NH = 1) or 4 of 48 KB (NH = 2)
 constexpr int MAX_STAGES = 6;
 constexpr int EPI_WARPS = 8;
+constexpr int SEG = TN / 2;               // columns of a segment (one epilogue group's) of the logits
 constexpr int E_BYTES = 32 * 64;          // 32 rows of 32 bf16 on their way out, two buffers per warp
 constexpr int OFF_E = RING_BYTES;
 constexpr int OFF_BAR = OFF_E + EPI_WARPS * 2 * E_BYTES;
@@ -53,6 +57,12 @@ constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignme
 constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int kNoTarget = 0x7fffffff;
+// Stages whose products a logit's accumulator takes before it is emptied into
+// fp32 registers (16: 1024 of the contraction).  The tensor core truncates every
+// addition to an accumulator, always towards 0, so a long sum drifts with its
+// length: the loss of a 4096-wide head was off by 1.4e-6 of its size, with
+// additions rounded to nearest every 1024 by LOSS_ERR.
+constexpr int CHUNK = 16;
 
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 
@@ -74,8 +84,8 @@ struct HeadGrid {
   int mtiles, ntiles;         // token tiles of 256, output tiles of tn
   int nwhole, ntail, nsplit;
   int band;                   // token tiles walked together
-  int nh;                     // accumulators per tile, side by side along the outputs
-  int bn;                     // outputs per accumulator (a multiple of 32; 256 if nh = 2 or MODE 1)
+  int nh;                     // accumulators per tile, side by side along the outputs (2: MODE 1 only)
+  int bn;                     // outputs per accumulator (a multiple of 32; 256 in MODE 1)
   int tn;                     // outputs per tile, nh bn
   int sw;                     // outputs of the first of a tile's two column segments (one per epilogue group)
 };
@@ -94,6 +104,17 @@ __device__ __forceinline__ uint32_t tmem_ld_one(uint32_t taddr) {
   return r;
 }
 
+// Two gradient values of a row with factors f (rscale): sums v0, v1 and a pair of
+// bf16 of the label's row of W.
+__device__ __forceinline__ uint32_t grad_pair(float v0, float v1, const float4& f, uint32_t w) {
+  if (f.y == 0.0f) return 0u;
+  return bf16x2_bits(fmaf(f.z, __uint_as_float(w << 16), v0 * f.x * f.y),
+                     fmaf(f.z, __uint_as_float(w & 0xffff0000u), v1 * f.x * f.y));
+}
+
+// Parts of a logit's contraction of n stages (accumulators it fills in turn).
+__device__ __forceinline__ int chunks(int n) { return (n + CHUNK - 1) / CHUNK; }
+
 // D = A B^T by pairs of CTAs (cta_group::2): 256 tokens x NH accumulators of up
 // to 256 outputs per tile, each CTA holding 128 token rows and half of the
 // output rows of each stage, both brought by TMA.  MODE 0: A = X, B = W
@@ -101,7 +122,7 @@ __device__ __forceinline__ uint32_t tmem_ld_one(uint32_t taddr) {
 // contraction (MN-major).
 //
 // A persistent pair walks its items.  NH = 1: two accumulators alternate, so the
-// epilogue of one tile runs under the products of the next.  NH = 2: the two
+// epilogue of one runs under the products of the next.  NH = 2 (MODE 1): the two
 // accumulators make one tile of 512 outputs, which brings a quarter fewer bytes
 // from L2 per product.
 //   warp 0     TMA producer
@@ -187,21 +208,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint32_t bytes = 2 * (UM + NH * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
-      const uint32_t full_at_leader = mapa_shared(full(0), 0);
-      bool ok = true, issued = false;
-      RingPos r;
-      for (int i = first; i < nitems && ok; i += step) {
-        int mt, nt, kbeg, kend, tail, z;
-        item(i, mt, nt, kbeg, kend, tail, z);
-        const int m0 = mt * TM + static_cast<int>(rank) * UM, n0 = nt * g.tn + static_cast<int>(rank) * bnl;
-        for (int k = kbeg; k < kend; ++k) {
-          const int s = r.slot;
-          if (!(ok = wait_bounded(empty(s), r.phase ^ 1, abort, status))) break;
-          issued = true;
-          if (leader) mbar_arrive_expect_tx(full(s), bytes);
-          const uint32_t bar = full_at_leader + 8u * s, a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
+    const uint32_t bytes = 2 * (UM + NH * bnl) * static_cast<uint32_t>(BK * 2);  // of both CTAs
+    const uint32_t full_at_leader = mapa_shared(full(0), 0);
+    bool ok = true, issued = false;
+    RingPos r;
+    for (int i = first; i < nitems && ok; i += step) {
+      int mt, nt, kbeg, kend, tail, z;
+      item(i, mt, nt, kbeg, kend, tail, z);
+      const int m0 = mt * TM + static_cast<int>(rank) * UM, n0 = nt * g.tn + static_cast<int>(rank) * bnl;
+      for (int k = kbeg; k < kend; ++k, r.advance(1, STAGES)) {
+        if (!(ok = wait_warp(empty(r.slot), r.phase ^ 1, abort, status))) break;
+        issued = true;
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(full(r.slot), bytes);
+          const uint32_t bar = full_at_leader + 8u * r.slot, a_s = base + r.slot * STAGE_BYTES, b_s = a_s + A_BYTES;
           tma_load_2d_pair(a_s, &tm_a, bar, k * BK, m0);
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
@@ -212,72 +232,79 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               tma_load_2d_pair(b_s + h * B_BYTES + 8192, &tm_b, bar, n0 + h * TN + 64, k * BK);
             }
           }
-          r.advance(1, STAGES);
         }
+        __syncwarp();
       }
-      // Let the copies already issued land before the CTA exits.  They report to
-      // the leader, which cannot see the end of a stage that only one CTA has
-      // issued, so each CTA gives its own the time they can need at most.
-      if (!ok && issued) {
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 20000000ull) {
-        }
+    }
+    // Let the copies already issued land before the CTA exits.  They report to
+    // the leader, which cannot see the end of a stage that only one CTA has
+    // issued, so each CTA gives its own the time they can need at most.
+    if (!ok && issued) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 20000000ull) {
       }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    if (leader && lane == 0) {
+    if (leader) {
       const uint32_t idesc = idesc_bf16(TM, g.bn, false, MODE == 1);
       bool ok = true, committed = false;
       RingPos r;
-      int t = 0;  // tiles so far
-      for (int i = first; i < nitems && ok; i += step, ++t) {
+      int t = 0;  // accumulators filled so far
+      for (int i = first; i < nitems && ok; i += step) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
-        if (NH == 1) {
-          ok = wait_bounded_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status);
-        } else {
-          ok = wait_bounded_cluster(acc_empty(0), (t & 1) ^ 1, abort, status) &&
-               wait_bounded_cluster(acc_empty(1), (t & 1) ^ 1, abort, status);
-        }
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = NH == 1 ? tmem + 256u * (t & 1) : tmem;
-        for (int k = kbeg; k < kend; ++k, r.advance(1, STAGES)) {
-          const int s = r.slot;
-          if (!(ok = wait_bounded_cluster(full(s), r.phase, abort, status))) break;
+        const int parts = MODE == 0 ? chunks(kend - kbeg) : 1;
+        for (int q = 0, k = kbeg; q < parts && ok; ++q, ++t) {
+          const int stop = kbeg + (q + 1) * (kend - kbeg) / parts, start = k;
+          if (NH == 1) {
+            ok = wait_warp_cluster(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status);
+          } else {
+            ok = wait_warp_cluster(acc_empty(0), (t & 1) ^ 1, abort, status) &&
+                 wait_warp_cluster(acc_empty(1), (t & 1) ^ 1, abort, status);
+          }
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_s = base + s * STAGE_BYTES, b_s = a_s + A_BYTES;
+          const uint32_t d = NH == 1 ? tmem + 256u * (t & 1) : tmem;
+          for (; k < stop; ++k, r.advance(1, STAGES)) {
+            if (!(ok = wait_warp_cluster(full(r.slot), r.phase, abort, status))) break;
+            tc_fence_after();
+            const uint32_t a_s = base + r.slot * STAGE_BYTES, b_s = a_s + A_BYTES;
+            const uint64_t ad = desc_sw128(a_s, 16, 1024);
+            const uint64_t bd = MODE == 0 ? desc_sw128(b_s, 16, 1024) : desc_sw128(b_s, 8192, 1024);
+            if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              const uint32_t b_h = b_s + h * B_BYTES;
-              const uint64_t bd =
-                  MODE == 0 ? desc_sw128(b_h + kk * 32, 16, 1024) : desc_sw128(b_h + kk * 2048, 8192, 1024);
-              const uint64_t ad = desc_sw128(a_s + kk * 32, 16, 1024);
-              const uint32_t more = (k > kbeg || kk > 0) ? 1u : 0u;
-              if (NH == 1) tc_mma_f16_pair(d, ad, bd, idesc, more);
-              else if (h == 0) tc_mma_f16_pair_fill_a(d, ad, bd, idesc, more);
-              else tc_mma_f16_pair_last_a(d + 256u, ad, bd, idesc, more);
+              for (int kk = 0; kk < BK / 16; ++kk) {  // a descriptor's low bits are the address / 16
+                const uint64_t a_k = ad + kk * 2, b_k = bd + kk * (MODE == 0 ? 2 : 128);
+                const uint32_t more = (k > start || kk > 0) ? 1u : 0u;
+                if (NH == 1) {
+                  tc_mma_f16_pair(d, a_k, b_k, idesc, more);
+                } else {
+                  tc_mma_f16_pair_fill_a(d, a_k, b_k, idesc, more);
+                  tc_mma_f16_pair_last_a(d + 256u, a_k, b_k + B_BYTES / 16, idesc, more);
+                }
+              }
+              tc_commit_pair(empty(r.slot));
+            }
+            __syncwarp();
+            committed = true;
+          }
+          if (ok && elect_one()) {
+            if (NH == 1) {
+              tc_commit_pair(acc_full(t & 1));
+            } else {
+              tc_commit_pair(acc_full(0));
+              tc_commit_pair(acc_full(1));
             }
           }
-          tc_commit_pair(empty(s));
-          committed = true;
-        }
-        if (ok) {
-          if (NH == 1) {
-            tc_commit_pair(acc_full(t & 1));
-          } else {
-            tc_commit_pair(acc_full(0));
-            tc_commit_pair(acc_full(1));
-          }
+          __syncwarp();
         }
       }
-      if (!ok && committed) {  // wait for MMAs in flight before TMEM is freed
+      if (!ok && committed && elect_one()) {  // wait for MMAs in flight before TMEM is freed
         tc_commit_pair(drain_bar);
         wait_drain(drain_bar, 0);
       }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------- epilogue
@@ -289,54 +316,112 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int cwidth = h == 0 ? g.sw : g.tn - g.sw;    // and its width
     const uint32_t e_buf = base + OFF_E + static_cast<uint32_t>(warp - 2) * 2 * E_BYTES;
     int t = 0, stored = 0;
-    for (int i = first; i < nitems; i += step, ++t) {
-      int mt, nt, kbeg, kend, tail, z;
-      item(i, mt, nt, kbeg, kend, tail, z);
+    // Waits for the next accumulator, and gives it back.
+    auto take = [&](int& a) {
+      a = NH == 1 ? (t & 1) : h;
+      const bool landed = wait_warp(acc_full(a), NH == 1 ? (t >> 1) & 1 : t & 1, abort, status);
+      ++t;
+      tc_fence_after();
+      return landed;
+    };
+    auto give = [&](int a) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(acc_empty(a));
+        else mbar_arrive_remote(empty_at_leader + 8u * a);
+      }
+    };
+    bool ok = true;
+    for (int i = first; i < nitems && ok; i += step) {
+      int mt, nt, kbeg, kend, tail, zp;
+      item(i, mt, nt, kbeg, kend, tail, zp);
       const int row0 = mt * TM + static_cast<int>(rank) * UM + quad * 32;  // the warp's first row
       const int row = row0 + lane;
       const int n0 = nt * g.tn + cseg;  // the segment's first output
-      const int a = NH == 1 ? (t & 1) : h;
-      const bool landed = wait_bounded(acc_full(a), NH == 1 ? (t >> 1) & 1 : t & 1, abort, status);
-      if (!__all_sync(0xffffffffu, landed)) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + lane_base + (NH == 1 ? 256u * a + cseg : 256u * h);
-      if (MODE == 0 && row0 < p.rows) {
-        const bool live = row < p.rows;
+      const bool used = row0 < p.rows, live = row < p.rows;
+      int a;
+      if (MODE == 0) {
         const int ncols = max(0, min(cwidth, p.cols - n0));
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int col = 0; col < ncols; col += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(acc + col, v);
-          tmem_ld_wait();
-          if (col + 32 <= ncols) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j < ncols) mx = fmaxf(mx, __uint_as_float(v[j]));
-          }
+        // The targets of the thread's row in this segment, in ascending order.
+        int first_t = 0, end_t = 0;
+        float zt = 0.0f;  // cross entropy: the label's logit
+        if (live && p.labels) {
+          const int64_t y = p.labels[row];
+          end_t = y >= n0 && y < n0 + ncols;
+        } else if (live) {
+          const uint16_t* o = p.off + static_cast<int64_t>(row) * (2 * g.ntiles + 1) + 2 * nt + h;
+          first_t = o[0];
+          end_t = o[1];
         }
+        float2* ztgt = p.ztgt + static_cast<int64_t>(row) * p.k;
+        auto entry = [&](int j) {
+          return p.labels ? static_cast<int>(p.labels[row]) : p.sidx[static_cast<int64_t>(row) * p.k + j];
+        };
+        float z[SEG];
+        const int parts = chunks(kend - kbeg);
+        for (int q = 0; q < parts; ++q) {
+          if (!(ok = take(a))) break;
+          const uint32_t acc = tmem + lane_base + 256u * a + cseg;
+          if (used) {
+#pragma unroll
+            for (int c = 0; c < SEG; c += 16) {
+              if (c < cwidth) {
+                uint32_t v[16];
+                tmem_ld_x16(acc + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  z[c + j] = q == 0 ? __uint_as_float(v[j]) : z[c + j] + __uint_as_float(v[j]);
+              }
+            }
+            // Target logits: the warp visits the columns that any of its rows wants,
+            // in ascending order (at most a segment of them, usually none or a few).
+            int cur = first_t, want = cur < end_t ? entry(cur) : kNoTarget;
+            for (;;) {
+              const int c = __reduce_min_sync(0xffffffffu, want);
+              if (c == kNoTarget) break;
+              const float v = __uint_as_float(tmem_ld_one(acc + (c - n0)));
+              tmem_ld_wait();
+              if (want == c) {
+                if (p.labels) zt += v;
+                else ztgt[cur].x = q == 0 ? v : ztgt[cur].x + v;
+                ++cur;
+                want = cur < end_t ? entry(cur) : kNoTarget;
+              }
+            }
+          }
+          give(a);  // the rest runs beside the products of the next accumulator
+        }
+        if (!ok) break;
+        if (!used) continue;
+        if (ncols < SEG) {
+#pragma unroll
+          for (int j = 0; j < SEG; ++j)
+            if (j >= ncols) z[j] = -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < SEG; ++j) mx = fmaxf(mx, z[j]);
         // The segment's reference in units of log2 is a whole number, so taking it
         // off and putting it back are exact.  (A segment whose logits are all -inf
         // or NaN is summed around 0.)
         const float ref = mx == -INFINITY ? 0.0f : rintf(mx * p.c);
         const float back = exp2f(fabsf(ref) <= kHeadFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
         const __nv_bfloat162 back2 = __float2bfloat162_rn(back);
+        if (p.labels) {
+          if (end_t) ztgt[0] = make_float2(fmaf(zt, p.c, -ref), ref);
+        } else {
+          for (int j = first_t; j < end_t; ++j) ztgt[j] = make_float2(fmaf(ztgt[j].x, p.c, -ref), ref);
+        }
         float sum = 0.0f;
         const int ewidth = static_cast<int>(min(static_cast<int64_t>(cwidth), p.lde - n0));
-#pragma unroll 1
-        for (int col = 0; col < ewidth; col += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(acc + col, v);
-          tmem_ld_wait();
-          float e[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), p.c, -ref));
-            if (col + 32 > ncols && col + j >= ncols) e[j] = 0.0f;
-          }
+        for (int col = 0; col < SEG; col += 32) {
+          if (col >= ewidth) break;
+          float* e = z + col;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) e[j] = exp2_fast(fmaf(e[j], p.c, -ref));
           if (p.e) {
             // 32 rows x 32 columns through shared memory (64-byte swizzle) and out by
             // TMA: written from the registers, every 16 bytes of a lane would be a
@@ -362,7 +447,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             ++stored;
           }
-          // As a tree: a column with p near 1 then meets the small rest in 13
+          // As a tree: a column with p near 1 then meets the small rest in 9
           // additions at most per segment, not in one for each of them (a loss of
           // 1e-5 is the difference of the sum from 1).
 #pragma unroll
@@ -376,69 +461,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             *reinterpret_cast<uint4*>(p.e + static_cast<int64_t>(row) * p.lde + col) = make_uint4(0u, 0u, 0u, 0u);
         if (live)
           p.part[(2 * static_cast<int64_t>(nt) + h) * p.rows + row] = make_float2(mx == -INFINITY ? mx : ref, sum);
-        // Target logits: the warp visits the columns that any of its rows wants,
-        // in ascending order (at most a segment of them, usually none or a few).
-        int cur = 0, end = 0, want = kNoTarget;
-        if (live) {
-          if (p.labels) {
-            const int64_t y = p.labels[row];
-            if (y >= n0 && y < n0 + ncols) {
-              want = static_cast<int>(y);
-              end = 1;
-            }
-          } else {
-            const uint16_t* o = p.off + static_cast<int64_t>(row) * (2 * g.ntiles + 1) + 2 * nt + h;
-            cur = o[0];
-            end = o[1];
-            if (cur < end) want = p.sidx[static_cast<int64_t>(row) * p.k + cur];
-          }
-        }
-        for (;;) {
-          const int c = __reduce_min_sync(0xffffffffu, want);
-          if (c == kNoTarget) break;
-          const uint32_t v = tmem_ld_one(acc + (c - n0));
-          tmem_ld_wait();
-          if (want == c) {
-            p.ztgt[static_cast<int64_t>(row) * p.k + cur] =
-                make_float2(fmaf(__uint_as_float(v), p.c, -ref), ref);
-            ++cur;
-            want = cur < end ? p.sidx[static_cast<int64_t>(row) * p.k + cur] : kNoTarget;
-          }
-        }
-      }
-      if (MODE == 1 && row0 < p.rows) {
-        const bool live = row < p.rows;
-        const float2 f = live && tail < 0 ? p.rscale[row] : make_float2(0.0f, 0.0f);
+      } else {
+        if (!(ok = take(a))) break;
+        const uint32_t acc = tmem + lane_base + (NH == 1 ? 256u * a + cseg : 256u * h);
+        if (used) {
+          const float4 f = live && tail < 0 ? p.rscale[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const int label = live && tail < 0 ? __float_as_int(f.w) : -1;
+          const uint16_t* wl = label >= 0 ? p.W + static_cast<int64_t>(label) * p.cols + n0 : nullptr;
 #pragma unroll 1
-        for (int col = 0; col < cwidth && n0 + col < p.cols; col += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(acc + col, v);
-          tmem_ld_wait();
-          if (tail >= 0) {  // a piece of a split tile: fp32 sums, joined by k_head_join
-            float4* dst = reinterpret_cast<float4*>(
-                p.split +
-                ((static_cast<int64_t>(tail) * g.nsplit + z) * TM + rank * UM + quad * 32 + lane) * g.tn + cseg + col);
+          for (int col = 0; col < cwidth && n0 + col < p.cols; col += 32) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc + col, v);
+            uint4 w[4] = {};  // the label's row of W
+            if (wl) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-          } else if (live) {
-            float x[32];
+              for (int q = 0; q < 4; ++q) w[q] = ldg_nc_v4(wl + col + 8 * q);
+            }
+            tmem_ld_wait();
+            if (tail >= 0) {  // a piece of a split tile: fp32 sums, joined by k_head_join
+              float4* dst = reinterpret_cast<float4*>(
+                  p.split + ((static_cast<int64_t>(tail) * g.nsplit + zp) * TM + rank * UM + quad * 32 + lane) * g.tn +
+                  cseg + col);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = f.y == 0.0f ? 0.0f : __uint_as_float(v[j]) * f.x * f.y;
-            uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n0 + col);
+              for (int q = 0; q < 8; ++q)
+                dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                     __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+            } else if (live) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n0 + col);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)  // cols % 64 == 0: a group of 32 columns is whole
-              dst[q] = make_uint4(bf16x2_bits(x[8 * q], x[8 * q + 1]), bf16x2_bits(x[8 * q + 2], x[8 * q + 3]),
-                                  bf16x2_bits(x[8 * q + 4], x[8 * q + 5]), bf16x2_bits(x[8 * q + 6], x[8 * q + 7]));
+              for (int q = 0; q < 4; ++q) {  // cols % 64 == 0: a group of 32 columns is whole
+                const uint32_t wq[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  o[j] = grad_pair(__uint_as_float(v[8 * q + 2 * j]), __uint_as_float(v[8 * q + 2 * j + 1]), f, wq[j]);
+                dst[q] = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(acc_empty(a));
-        else mbar_arrive_remote(empty_at_leader + 8u * a);
+        give(a);
       }
     }
     if (MODE == 0 && lane == 0) bulk_wait_all();  // the stores have left shared memory and are visible
@@ -488,12 +550,13 @@ __global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ spl
     b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
     src += TM * g.tn;
   }
-  const float2 f = p.rscale[row];
-  uint4 o = make_uint4(0u, 0u, 0u, 0u);
-  if (f.y != 0.0f)
-    o = make_uint4(bf16x2_bits(a.x * f.x * f.y, a.y * f.x * f.y), bf16x2_bits(a.z * f.x * f.y, a.w * f.x * f.y),
-                   bf16x2_bits(b.x * f.x * f.y, b.y * f.x * f.y), bf16x2_bits(b.z * f.x * f.y, b.w * f.x * f.y));
-  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n) = o;
+  const float4 f = p.rscale[row];
+  const int label = __float_as_int(f.w);
+  uint4 lw = make_uint4(0u, 0u, 0u, 0u);
+  if (label >= 0) lw = ldg_nc_v4(p.W + static_cast<int64_t>(label) * p.cols + n);
+  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n) =
+      make_uint4(grad_pair(a.x, a.y, f, lw.x), grad_pair(a.z, a.w, f, lw.y), grad_pair(b.x, b.y, f, lw.z),
+                 grad_pair(b.z, b.w, f, lw.w));
 }
 
 // The teacher's slots of one row per block: the softmax of the kept logits over
@@ -560,20 +623,16 @@ struct RowStat {
   int rescale;  // some segment is stored relative to its own reference
 };
 
-// Writes p - q, relative to reference r, into the row's target columns (one warp
-// per row).  Cross entropy: p - 1 = expm1(-loss).
+// Writes the row's target columns (one warp per row): 0 for a label, whose p - 1
+// the gradient's epilogue adds; p - q relative to reference r for a teacher's.
 __device__ __forceinline__ void write_targets(uint16_t* er, const RowStat& st, int lane, const int64_t* labels,
                                               int row, const int* sidx, const float* logq, int k,
                                               const float2* ztgt) {
-  const float up = exp2f((st.m - st.r) + st.l2s);
   if (labels) {
-    if (lane == 0) {
-      const float2 z = ztgt[row];
-      const float d = expm1f(((z.x + (z.y - st.m)) - st.l2s) * kLn2) * up;
-      er[labels[row]] = static_cast<uint16_t>(bf16x2_bits(d, 0.0f));
-    }
+    if (lane == 0) er[labels[row]] = 0;
     return;
   }
+  const float up = exp2f((st.m - st.r) + st.l2s);
   const int64_t at = static_cast<int64_t>(row) * k;
   for (int j = lane; j < k; j += 32) {
     const int y = sidx[at + j];
@@ -595,7 +654,7 @@ __global__ void __launch_bounds__(SROWS * SLANES)
     k_head_stats(const float2* __restrict__ part, int nseg, int rows, int N, const int64_t* __restrict__ labels,
                  const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float2* __restrict__ ztgt,
                  float temp, const float* __restrict__ dloss, float* __restrict__ loss, float* __restrict__ lse,
-                 RowStat* __restrict__ stat, float2* __restrict__ rscale, uint16_t* __restrict__ e, int64_t lde) {
+                 RowStat* __restrict__ stat, float4* __restrict__ rscale, uint16_t* __restrict__ e, int64_t lde) {
   pdl_trigger();
   pdl_wait();
   __shared__ float2 sh[SROWS][SLANES + 1];
@@ -657,7 +716,10 @@ __global__ void __launch_bounds__(SROWS * SLANES)
     lse[row] = (m + st.l2s) * kLn2;
     if (e) {
       stat[row] = st;
-      rscale[row] = make_float2(exp2f(-((m - st.r) + st.l2s)), g);
+      // cross entropy: p - 1 = expm1(-loss) at the label
+      const float d = labels && any ? expm1f(-part_loss) * g : 0.0f;
+      rscale[row] = make_float4(exp2f(-((m - st.r) + st.l2s)), g, d,
+                                __int_as_float(labels && any ? static_cast<int>(labels[row]) : -1));
     }
   }
   if (e && g != 0.0f && !big)
@@ -673,7 +735,7 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
 // usually no row is marked, which its threads see in one look at 256 of them.
 __global__ void __launch_bounds__(256)
     k_head_rescale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int tn, int sw, int nseg,
-                   int rows, const RowStat* __restrict__ stat, const float2* __restrict__ rscale,
+                   int rows, const RowStat* __restrict__ stat, const float4* __restrict__ rscale,
                    const int64_t* __restrict__ labels, const int* __restrict__ sidx, const float* __restrict__ logq,
                    int k, const float2* __restrict__ ztgt) {
   pdl_trigger();
@@ -768,15 +830,12 @@ int band_of(int64_t mtiles, int64_t contraction) {
 // per CTA are 64 B per cycle, about what L2 delivers, so narrower tiles only pay
 // where they save a round.  With a single token tile the head's rows alone count
 // (they come from HBM): 32000 entries are two rounds of 256 on 74 pairs, or two
-// of 224.  A tile of 512 (two accumulators, whose epilogue no other tile's
-// products cover) takes 0.913 of the time per stage and about 7 stages more per
-// 256 outputs: measured 0.97 of the time at K = 8192, 1.02 at 4096.
+// of 224.
 HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
   HeadGrid g{};
   g.mtiles = static_cast<int>((rows + TM - 1) / TM);
   g.bn = TN;
   const int P = head_pairs();
-  const double numK = static_cast<double>((K + BK - 1) / BK);
   g.nh = 1;
   if (P > 0) {
     double best = 0.0;
@@ -788,15 +847,9 @@ HeadGrid logits_grid(int64_t rows, int64_t N, int64_t K) {
         g.bn = bn;
       }
     }
-    const int64_t rounds = (g.mtiles * ((N + 2 * TN - 1) / (2 * TN)) + P - 1) / P;
-    const double cost = static_cast<double>(rounds) * TN * 2 * (0.913 + 6.8 / numK);
-    if (g.mtiles > 1 && cost < best) {
-      g.nh = 2;
-      g.bn = TN;
-    }
   }
   g.tn = g.nh * g.bn;
-  g.sw = g.nh == 2 ? TN : std::min(g.bn, TN / 2);
+  g.sw = std::min(g.bn, SEG);
   g.ntiles = static_cast<int>((N + g.tn - 1) / g.tn);
   g.nwhole = g.mtiles * g.ntiles;
   g.nsplit = 1;
@@ -882,7 +935,8 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct HeadSpace {
   uint16_t* w16;
   float2* part;
-  float2 *ztgt, *rscale;
+  float2* ztgt;
+  float4* rscale;
   RowStat* stat;
   float *logq, *split;
   int* sidx;
@@ -913,7 +967,7 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
   }
   if (grad) {
     s.stat = static_cast<RowStat*>(take(static_cast<size_t>(rows) * sizeof(RowStat)));
-    s.rscale = static_cast<float2*>(take(static_cast<size_t>(rows) * 8));
+    s.rscale = static_cast<float4*>(take(static_cast<size_t>(rows) * 16));
     s.e = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * e_pitch(N) * 2));
     s.split = static_cast<float*>(take(std::max(split_bytes(rows, N, K), split_bytes(last, N, K))));
   }
@@ -1016,7 +1070,6 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
       if (err != cudaSuccess) return err;
     }
     if (few) err = launch_few_logits(h, X, seg.sw, p, st);
-    else if (g.nh == 2) err = launch_pairs<0, 2>(ma, mb, me, a.K, g, p, st);
     else err = launch_pairs<0, 1>(ma, mb, me, a.K, g, p, st);
     if (err != cudaSuccess) return err;
     err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
@@ -1029,7 +1082,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     if (!grad) continue;
     err = launch_ex(k_head_rescale, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 4 * device_sm_count()))),
                     dim3(256), 0, st, true, s.e, lde, static_cast<const float2*>(s.part), seg.tn, seg.sw, seg.count,
-                    p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float2*>(s.rscale), p.labels,
+                    p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float4*>(s.rscale), p.labels,
                     static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
                     static_cast<const float2*>(s.ztgt));
     if (err != cudaSuccess) return err;
@@ -1037,6 +1090,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     q.rows = p.rows;
     q.cols = static_cast<int>(a.K);
     q.rscale = s.rscale;
+    q.W = h.W;
     q.out = a.dX + r0 * a.K;
     q.split = s.split;
     if (few) {

@@ -33,8 +33,9 @@ struct HeadEpi {
   const uint16_t* off;       // [rows][segments + 1] first target of each column segment
   int k;
   float2* ztgt;              // [rows][k] target logits: (z c - n, n)
-  // MODE 1
-  const float2* rscale;      // [rows] factors (x, y) of the row (y = 0: the row is written as zeros)
+  // MODE 1: dX = sums x y + z W[w]; y = 0: the row is written as zeros; w < 0: no such term
+  const float4* rscale;      // [rows] (x, y, z, w as int)
+  const uint16_t* W;         // bf16 head (few tokens on an NF4 head: null)
   uint16_t* out;             // [rows][cols]
   float* split;              // fp32 sums of the split tiles' pieces
 };
@@ -47,6 +48,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // True in one lane of a converged warp.  The single-thread roles (TMA, MMA) run
 // with the whole warp and issue from the elected lane: their addresses and
 // descriptors are then the same in all lanes, as those instructions want them.

@@ -47,17 +47,10 @@ struct FewGrid {
   int numK;    // stages of the contraction (SUB x 64 each)
   int tp;      // tokens, rounded up to 16
   int stages;
+  int parts;   // accumulators that a contraction fills in turn
   int cols;    // TMEM columns
 };
 
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The same barrier; tells all 128 threads whether ok holds for every one of them.
 __device__ __forceinline__ bool epilogue_all(bool ok) {
@@ -193,20 +186,26 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       item(i, nt, z, kbeg, kend);
       if (!(ok = wait_warp(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
       tc_fence_after();
-      const uint32_t d = tmem + (t & 1) * g.tp;
+      const uint32_t d0 = tmem + (t & 1) * g.parts * g.tp;
+      int part = 0, start = kbeg;
       for (int k = kbeg; k < kend; ++k, r.advance(1, g.stages)) {
         if (!(ok = wait_warp(full(r.slot), r.phase, abort, status))) break;
         tc_fence_after();
         const uint32_t w_s = base + r.slot * stage_bytes, x_s = w_s + SUB * W_BYTES;
         const uint64_t ad = MODE == 0 ? desc_sw128(w_s, 16, 1024) : desc_sw128(w_s, 8192, 1024);
         const uint64_t bd = desc_sw128(x_s, 16, 1024);
+        if (part + 1 < g.parts && k == kbeg + (part + 1) * (kend - kbeg) / g.parts) {
+          ++part;
+          start = k;
+        }
+        const uint32_t d = d0 + part * g.tp;
         if (elect_one()) {
 #pragma unroll
           for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)  // a descriptor's low bits are the address / 16
               tc_mma_f16(d, ad + u * (W_BYTES / 16) + kk * (MODE == 0 ? 2 : 128), bd + u * (x_tile / 16) + kk * 2, idesc,
-                         (k > kbeg || u + kk > 0) ? 1u : 0u);
+                         (k > start || u + kk > 0) ? 1u : 0u);
           tc_commit(empty(r.slot));
         }
         __syncwarp();
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       // the four warps leave together: they meet at barriers
       if (!epilogue_all(wait_bounded(acc_full(t & 1), (t >> 1) & 1, abort, status))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + lane_base + (t & 1) * g.tp;
+      const uint32_t acc = tmem + lane_base + (t & 1) * g.parts * g.tp;
       if (MODE == 1) {
         const int k = nt * UM + quad * 32 + lane;
         float* dst = p.split + static_cast<int64_t>(z) * tokens * p.cols + k;
@@ -256,11 +255,15 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
           // has a token's entries side by side
           const uint32_t b = buf + (filled & 1) * (BUF_BYTES / 2);
           float* bp = reinterpret_cast<float*>(smem_raw + (b - raw));
-          uint32_t v[16];
-          tmem_ld_x16(acc + m, v);
-          tmem_ld_wait();
+          for (int q = 0; q < g.parts; ++q) {
+            uint32_t v[16];
+            tmem_ld_x16(acc + q * g.tp + m, v);
+            tmem_ld_wait();
+            float* x = bp + quad * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < BUF_TOKENS; ++j) bp[j * BUF_PITCH + quad * 32 + lane] = __uint_as_float(v[j]);
+            for (int j = 0; j < BUF_TOKENS; ++j)
+              x[j * BUF_PITCH] = q == 0 ? __uint_as_float(v[j]) : x[j * BUF_PITCH] + __uint_as_float(v[j]);
+          }
           epilogue_barrier();
           // The warp's four tokens together: each step is a chain of shuffles.
           constexpr int TW = BUF_TOKENS / 4;
@@ -447,9 +450,12 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
   }
 }
 
-// Sum of the gradient's pieces in piece order, times the row's factors, rounded
-// once to bf16.  Thread: 4 consecutive outputs of a token.
-__global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ split, int nsplit, HeadEpi p) {
+// Sum of the gradient's pieces in piece order, times the row's factors, plus the
+// label's term, rounded once to bf16.  Thread: 4 consecutive outputs of a token.
+__global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ split, int nsplit, HeadEpi p,
+                                                  const uint8_t* __restrict__ codes,
+                                                  const uint8_t* __restrict__ absmax_q,
+                                                  const float* __restrict__ dq_scale, Nf4Levels lv, int lg, int dq) {
   pdl_trigger();
   pdl_wait();
   const int c = (blockIdx.x * 128 + threadIdx.x) * 4, row = blockIdx.y;
@@ -461,9 +467,28 @@ __global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ spli
     const float4 x = *reinterpret_cast<const float4*>(split + at + z * piece);
     a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
   }
-  const float2 f = p.rscale[row];
+  const float4 f = p.rscale[row];
+  const int label = __float_as_int(f.w);
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // of the label's row of the head
+  if (label >= 0) {
+    const int64_t from = static_cast<int64_t>(label) * p.cols + c;
+    if (p.W) {
+      const uint2 b = *reinterpret_cast<const uint2*>(p.W + from);
+      w[0] = __uint_as_float(b.x << 16), w[1] = __uint_as_float(b.x & 0xffff0000u);
+      w[2] = __uint_as_float(b.y << 16), w[3] = __uint_as_float(b.y & 0xffff0000u);
+    } else {  // the four weights lie in one block
+      const int64_t blk = from >> lg;
+      const float scale = dq ? __fmul_rn(static_cast<float>(absmax_q[blk]), dq_scale[blk >> 8]) : dq_scale[blk];
+      const uint32_t b = *reinterpret_cast<const uint16_t*>(codes + from / 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = __bfloat162float(__float2bfloat16_rn(__fmul_rn(lv.v[(b >> (4 * j)) & 15u], scale)));
+    }
+  }
   uint2 o = make_uint2(0u, 0u);
-  if (f.y != 0.0f) o = make_uint2(bf16x2_bits(a.x * f.x * f.y, a.y * f.x * f.y), bf16x2_bits(a.z * f.x * f.y, a.w * f.x * f.y));
+  if (f.y != 0.0f)
+    o = make_uint2(bf16x2_bits(fmaf(f.z, w[0], a.x * f.x * f.y), fmaf(f.z, w[1], a.y * f.x * f.y)),
+                   bf16x2_bits(fmaf(f.z, w[2], a.z * f.x * f.y), fmaf(f.z, w[3], a.w * f.x * f.y)));
   *reinterpret_cast<uint2*>(p.out + at) = o;
 }
 
@@ -476,12 +501,15 @@ int few_smem(const FewGrid& g) {
   return 1024 + g.stages * SUB * (W_BYTES + g.tp * BK * 2) + BUF_BYTES + BAR_BYTES;
 }
 
-FewGrid few_grid(int64_t tokens) {
+FewGrid few_grid(int64_t tokens, int parts) {
   FewGrid g{};
   g.tp = static_cast<int>((tokens + 15) / 16 * 16);
   g.stages = few_stages(g.tp);
+  // As many accumulators as the contraction has thousands, while two sets fit
+  // TMEM (see CHUNK in head.cu).
+  g.parts = std::max(1, std::min(parts, 256 / g.tp));
   g.cols = 32;
-  while (g.cols < 2 * g.tp) g.cols *= 2;
+  while (g.cols < 2 * g.parts * g.tp) g.cols *= 2;
   return g;
 }
 
@@ -546,7 +574,7 @@ int few_splits(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st) {
-  FewGrid g = few_grid(p.rows);
+  FewGrid g = few_grid(p.rows, static_cast<int>((h.K + 1023) / 1024));
   g.br = br;
   g.tiles = static_cast<int>((h.N + br - 1) / br);
   g.nsplit = 1;
@@ -559,7 +587,7 @@ cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, co
 
 cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp, int nsplit, const HeadEpi& p,
                             cudaStream_t st) {
-  FewGrid g = few_grid(p.rows);
+  FewGrid g = few_grid(p.rows, 1);
   g.br = UM;
   g.tiles = static_cast<int>((h.K + UM - 1) / UM);
   g.nsplit = nsplit;
@@ -567,10 +595,13 @@ cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp,
   CUtensorMap w{}, x;
   if ((h.W && !make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, 64, BK, SW128)) ||
       !make_map(&x, BF16, P, ldp, p.rows, ldp * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
+  int lg = 0;
+  while ((1 << lg) < h.block) ++lg;
   cudaError_t e = launch_few<1>(w, x, g, p, h, st);
   if (e != cudaSuccess) return e;
   return launch_ex(k_few_join, dim3(static_cast<unsigned>((p.cols + 511) / 512), static_cast<unsigned>(p.rows)),
-                   dim3(128), 0, st, true, static_cast<const float*>(p.split), nsplit, p);
+                   dim3(128), 0, st, true, static_cast<const float*>(p.split), nsplit, p, h.codes, h.absmax_q, h.dq_scale,
+                   host_codebook().levels, lg, h.dq_block ? 1 : 0);
 }
 
 }  // namespace qn

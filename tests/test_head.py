@@ -11,7 +11,8 @@ Tolerances.  u = 2^-24 is the fp32 rounding, b = 2^-8 the bf16 one.
    trees of 32 and over the tiles, log2, the product with ln 2) are fewer than
    64 roundings of terms no larger than |z| + |lse| + 1, plus 72 relative
    roundings of a sum of positive terms; the tolerance allows 160 u of that.
- - p is rounded once to bf16 (as e), and so is a target's p - q; both carry the
+ - p is rounded once to bf16 (as e), and so is a teacher's p - q (a label's p - 1
+   stays in fp32); both carry the
    logits' 2 D and the fp32 steps of the exponent.  Entries of e below 2^-126 are
    flushed to 0, and e is stored relative to a reference that is at most 2^64
    above the row's sum (or factors of at least 2^-149 bring a value of at most
@@ -209,13 +210,15 @@ def test_distill_crowded_targets(L, what):
 @gpu
 def test_distill_of_one_slot_is_cross_entropy(L):
     M, N, K = 300, 1111, 256
-    head, _, X, labels, g = make(5, M, N, K)
+    head, values, X, labels, g = make(5, M, N, K)
     labels[7] = -100
     dloss = torch.rand(M, generator=g).cuda()
     a = qb.qlora_head_xent(head, X, labels, dloss=dloss)
     b = qb.qlora_head_distill(head, X, labels[:, None].contiguous(), torch.zeros(M, 1, device="cuda"), 1.0, dloss=dloss)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
-    assert (a[2].float() - b[2].float()).norm() <= 1e-3 * a[2].float().norm()
+    ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)  # (the distillation rounds its p - q to bf16)
+    compare(a, ref)
+    compare(b, ref)
 
 
 @gpu
