@@ -17,10 +17,11 @@
 // p = e exp(-lse) is a factor of the whole row, so it waits for the epilogue,
 // and only the target columns of e change in between, because p - q from a rounded
 // p would be noise for a confident token: the teacher's hold p - q, computed from
-// their fp32 logits and rounded once; the label's holds 0, and its p - 1 times its
-// row of W is added in fp32 (it is most of the gradient, and p - 1 is -1 for most
-// tokens: rounded after the row's factor it alone made the error of dX 1.5 times
-// that of a bf16 result).  So a loss with its gradient costs two products and no pass over the
+// their fp32 logits and rounded once.  A label stays out of e and of the sums: its
+// p - 1 times its row of W is added in fp32 (it is most of the gradient, and p - 1
+// is -1 for most tokens: rounded after the row's factor it alone made the error of
+// dX 1.5 times that of a bf16 result), and the loss is log1p(exp(lse of the others
+// - label's logit)), which keeps the digits of a small loss.  So a loss with its gradient costs two products and no pass over the
 // exponentials.
 //  - Computing p from the logits a second time would need three products.
 //  - Keeping the logits themselves in bf16 would cost accuracy: a rounding error
@@ -58,11 +59,13 @@ constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int kNoTarget = 0x7fffffff;
 // Stages whose products a logit's accumulator takes before it is emptied into
-// fp32 registers (16: 1024 of the contraction).  The tensor core truncates every
+// fp32 registers (32: 2048 of the contraction).  The tensor core truncates every
 // addition to an accumulator, always towards 0, so a long sum drifts with its
-// length: the loss of a 4096-wide head was off by 1.4e-6 of its size, with
-// additions rounded to nearest every 1024 by LOSS_ERR.
-constexpr int CHUNK = 16;
+// length; the registers' additions round to nearest.  Error of the loss (relative,
+// 8 tokens) and time of the losses of 4096 x 32000 x 4096 / 2048 x 32000 x 8192:
+// every 16 stages 1.6e-7, 751 us / 2.3e-7, 740 us; every 32 3.0e-7, 661 us /
+// 5.4e-7, 695 us; never 6.8e-7, 646 us / 1.3e-6, 689 us.
+constexpr int CHUNK = 32;
 
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 
@@ -98,18 +101,19 @@ __device__ __forceinline__ void tile_of(const HeadGrid& g, int L, int& mt, int& 
   mt = b * g.band + (rem - nt * in_band);
 }
 
-__device__ __forceinline__ uint32_t tmem_ld_one(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  return r;
-}
-
 // Two gradient values of a row with factors f (rscale): sums v0, v1 and a pair of
 // bf16 of the label's row of W.
 __device__ __forceinline__ uint32_t grad_pair(float v0, float v1, const float4& f, uint32_t w) {
   if (f.y == 0.0f) return 0u;
   return bf16x2_bits(fmaf(f.z, __uint_as_float(w << 16), v0 * f.x * f.y),
                      fmaf(f.z, __uint_as_float(w & 0xffff0000u), v1 * f.x * f.y));
+}
+
+// Arrival at a barrier of the other CTA that orders no memory of this thread: what
+// it reports are TMEM loads, which have completed.  The releasing form waits for
+// the thread's earlier stores first.
+__device__ __forceinline__ void arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Parts of a logit's contraction of n stages (accumulators it fills in turn).
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         if (leader) mbar_arrive(acc_empty(a));
-        else mbar_arrive_remote(empty_at_leader + 8u * a);
+        else arrive_remote_relaxed(empty_at_leader + 8u * a);
       }
     };
     bool ok = true;
@@ -343,21 +347,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int a;
       if (MODE == 0) {
         const int ncols = max(0, min(cwidth, p.cols - n0));
-        // The targets of the thread's row in this segment, in ascending order.
-        int first_t = 0, end_t = 0;
-        float zt = 0.0f;  // cross entropy: the label's logit
+        // The row's label in this segment, or its teacher's slots in ascending order.
+        int label = kNoTarget, first_t = 0, end_t = 0;
         if (live && p.labels) {
-          const int64_t y = p.labels[row];
-          end_t = y >= n0 && y < n0 + ncols;
+          const int64_t y = p.labels[row] - n0;
+          if (y >= 0 && y < ncols) label = static_cast<int>(y);
         } else if (live) {
           const uint16_t* o = p.off + static_cast<int64_t>(row) * (2 * g.ntiles + 1) + 2 * nt + h;
           first_t = o[0];
           end_t = o[1];
         }
-        float2* ztgt = p.ztgt + static_cast<int64_t>(row) * p.k;
-        auto entry = [&](int j) {
-          return p.labels ? static_cast<int>(p.labels[row]) : p.sidx[static_cast<int64_t>(row) * p.k + j];
-        };
         float z[SEG];
         const int parts = chunks(kend - kbeg);
         for (int q = 0; q < parts; ++q) {
@@ -375,21 +374,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   z[c + j] = q == 0 ? __uint_as_float(v[j]) : z[c + j] + __uint_as_float(v[j]);
               }
             }
-            // Target logits: the warp visits the columns that any of its rows wants,
-            // in ascending order (at most a segment of them, usually none or a few).
-            int cur = first_t, want = cur < end_t ? entry(cur) : kNoTarget;
-            for (;;) {
-              const int c = __reduce_min_sync(0xffffffffu, want);
-              if (c == kNoTarget) break;
-              const float v = __uint_as_float(tmem_ld_one(acc + (c - n0)));
-              tmem_ld_wait();
-              if (want == c) {
-                if (p.labels) zt += v;
-                else ztgt[cur].x = q == 0 ? v : ztgt[cur].x + v;
-                ++cur;
-                want = cur < end_t ? entry(cur) : kNoTarget;
-              }
-            }
           }
           give(a);  // the rest runs beside the products of the next accumulator
         }
@@ -400,6 +384,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int j = 0; j < SEG; ++j)
             if (j >= ncols) z[j] = -INFINITY;
         }
+        if (__any_sync(0xffffffffu, label != kNoTarget)) {
+#pragma unroll
+          for (int j = 0; j < SEG; ++j)
+            if (label == j) z[j] = -INFINITY;
+        }
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < SEG; ++j) mx = fmaxf(mx, z[j]);
@@ -409,10 +398,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float ref = mx == -INFINITY ? 0.0f : rintf(mx * p.c);
         const float back = exp2f(fabsf(ref) <= kHeadFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
         const __nv_bfloat162 back2 = __float2bfloat162_rn(back);
-        if (p.labels) {
-          if (end_t) ztgt[0] = make_float2(fmaf(zt, p.c, -ref), ref);
-        } else {
-          for (int j = first_t; j < end_t; ++j) ztgt[j] = make_float2(fmaf(ztgt[j].x, p.c, -ref), ref);
+        // The teacher's slots, from the registers: only a warp with a slot in this
+        // segment looks for them.
+        if (__any_sync(0xffffffffu, first_t < end_t)) {
+          const int* idx = p.sidx + static_cast<int64_t>(row) * p.k;
+          int cur = first_t, want = cur < end_t ? idx[cur] - n0 : kNoTarget;
+#pragma unroll
+          for (int j = 0; j < SEG; ++j) {
+            while (want == j) {  // more than once for an entry in several slots
+              p.ztgt[static_cast<int64_t>(row) * p.k + cur] = make_float2(fmaf(z[j], p.c, -ref), ref);
+              ++cur;
+              want = cur < end_t ? idx[cur] - n0 : kNoTarget;
+            }
+          }
         }
         float sum = 0.0f;
         const int ewidth = static_cast<int>(min(static_cast<int64_t>(cwidth), p.lde - n0));
@@ -623,15 +621,10 @@ struct RowStat {
   int rescale;  // some segment is stored relative to its own reference
 };
 
-// Writes the row's target columns (one warp per row): 0 for a label, whose p - 1
-// the gradient's epilogue adds; p - q relative to reference r for a teacher's.
-__device__ __forceinline__ void write_targets(uint16_t* er, const RowStat& st, int lane, const int64_t* labels,
-                                              int row, const int* sidx, const float* logq, int k,
-                                              const float2* ztgt) {
-  if (labels) {
-    if (lane == 0) er[labels[row]] = 0;
-    return;
-  }
+// Writes p - q, relative to reference r, into the columns of the row's teacher
+// slots (one warp per row).
+__device__ __forceinline__ void write_targets(uint16_t* er, const RowStat& st, int lane, int row, const int* sidx,
+                                              const float* logq, int k, const float2* ztgt) {
   const float up = exp2f((st.m - st.r) + st.l2s);
   const int64_t at = static_cast<int64_t>(row) * k;
   for (int j = lane; j < k; j += 32) {
@@ -645,16 +638,44 @@ __device__ __forceinline__ void write_targets(uint16_t* er, const RowStat& st, i
   }
 }
 
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    s = fmaf(__uint_as_float(x[j] << 16), __uint_as_float(y[j] << 16), s);
+    s = fmaf(__uint_as_float(x[j] & 0xffff0000u), __uint_as_float(y[j] & 0xffff0000u), s);
+  }
+  return s;
+}
+
+// What k_head_stats reads and writes.
+struct StatArgs {
+  const float2* part;  // [nseg][rows]
+  int nseg, rows, N, K;
+  const int64_t* labels;           // cross entropy, with
+  const uint16_t *X, *W;           //   the label's logit computed here from these, or (null) in ztgt
+  const int* sidx;                 // distillation
+  const float* logq;
+  int k;
+  const float2* ztgt;
+  float c, temp;
+  const float* dloss;
+  float *loss, *lse;
+  RowStat* stat;
+  float4* rscale;
+  uint16_t* e;  // null: no gradient
+  int64_t lde;
+};
+
 // Joins the segments' (reference, sum) pairs of 8 rows per block: first thread
 // (r, j) takes row r and segments j, j + 64, ..., then warp r joins its row's 64
-// values, adds up its targets' terms of the loss and writes its target columns of
-// e.  The orders are fixed.
+// values, adds the label's logit or the teacher's terms of the loss, and writes the
+// teacher's columns of e.  The orders are fixed.  The label's logit is one more dot
+// product of X and W with fp32 additions rounded to nearest (12 us for 4096 x 4096,
+// read from HBM): the tensor core's truncating sum alone made the loss of 2047 x
+// 50003 x 2048 1.4e-6 off instead of 4e-7.
 constexpr int SROWS = 8, SLANES = 64;
-__global__ void __launch_bounds__(SROWS * SLANES)
-    k_head_stats(const float2* __restrict__ part, int nseg, int rows, int N, const int64_t* __restrict__ labels,
-                 const int* __restrict__ sidx, const float* __restrict__ logq, int k, const float2* __restrict__ ztgt,
-                 float temp, const float* __restrict__ dloss, float* __restrict__ loss, float* __restrict__ lse,
-                 RowStat* __restrict__ stat, float4* __restrict__ rscale, uint16_t* __restrict__ e, int64_t lde) {
+__global__ void __launch_bounds__(SROWS * SLANES) k_head_stats(const __grid_constant__ StatArgs p) {
   pdl_trigger();
   pdl_wait();
   __shared__ float2 sh[SROWS][SLANES + 1];
@@ -665,10 +686,10 @@ __global__ void __launch_bounds__(SROWS * SLANES)
   const int r = threadIdx.x % SROWS, seg0 = threadIdx.x / SROWS;
   if (threadIdx.x < SROWS) own[threadIdx.x] = 0;
   __syncthreads();
-  if (row0 + r < rows) {
+  if (row0 + r < p.rows) {
 #pragma unroll 4
-    for (int t = seg0; t < nseg; t += SLANES) {
-      const float2 v = part[static_cast<int64_t>(t) * rows + row0 + r];
+    for (int t = seg0; t < p.nseg; t += SLANES) {
+      const float2 v = p.part[static_cast<int64_t>(t) * p.rows + row0 + r];
       const float top = fmaxf(m, v.x);
       s = s * shift2(m, top) + v.y * shift2(v.x, top);
       m = top;
@@ -680,50 +701,72 @@ __global__ void __launch_bounds__(SROWS * SLANES)
   __syncthreads();
   const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
   const int row = row0 + b;
-  if (b >= SROWS || row >= rows) return;
+  if (b >= SROWS || row >= p.rows) return;
   const float2 v = sh[b][a], w = sh[b][a + 32];
   m = fmaxf(v.x, w.x);
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   s = v.y * shift2(v.x, m) + w.y * shift2(w.x, m);
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   big = own[b] != 0;
-  const RowStat st{m, log2f(s), big ? m : 0.0f, big ? 1 : 0};
-  // loss = T^2 sum_s q_s (log q_s + (lse - z_s)); lse - z_s in units of log2 is
-  // (m - n) - (z - n) + log2(sum), which keeps the digits of a small loss.
-  float part_loss = 0.0f;
+  RowStat st{m, 0.0f, big ? m : 0.0f, big ? 1 : 0};
+  float total = 0.0f, d = 0.0f;  // the loss / T^2, and the label's p - 1
   bool any = false;
-  if (labels) {
-    const int64_t y = labels[row];
-    any = y >= 0 && y < N;
-    if (any && a == 0) {
-      const float2 z = ztgt[row];
-      part_loss = (((m - z.y) - z.x) + st.l2s) * kLn2;
+  int label = -1;
+  if (p.labels) {
+    const int64_t y = p.labels[row];
+    any = y >= 0 && y < p.N;
+    if (any) {
+      label = static_cast<int>(y);
+      float zy;  // the label's logit times c, relative to ny
+      float ny;
+      if (p.X) {
+        const uint4* x = reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(row) * p.K);
+        const uint4* u = reinterpret_cast<const uint4*>(p.W + y * p.K);
+        float z = 0.0f;
+#pragma unroll 4
+        for (int j = a; j < p.K / 8; j += 32) z = dot8(x[j], u[j], z);
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        ny = rintf(z * p.c);
+        zy = fmaf(z, p.c, -ny);
+      } else {
+        const float2 z = p.ztgt[row];
+        zy = z.x;
+        ny = z.y;
+      }
+      // log2 of p / (1 - p): the sums hold the other entries alone
+      const float odds = (zy + (ny - m)) - log2f(s);
+      total = log1pf(exp2f(-fabsf(odds))) + (odds < 0.0f ? -odds * kLn2 : 0.0f);
+      d = expm1f(-total);
+      const float top = fmaxf(m, ny);
+      s = s * shift2(m, top) + exp2f(zy + (ny - top));
+      st.m = top;
     }
+    st.l2s = log2f(s);
   } else {
-    const int64_t at = static_cast<int64_t>(row) * k;
-    any = sidx[at] != kNoTarget;
-    for (int j = a; j < k; j += 32) {
-      if (sidx[at + j] == kNoTarget) break;
-      const float lq = logq[at + j], q = expf(lq);
-      const float2 z = ztgt[at + j];
-      if (q != 0.0f) part_loss += q * (lq + (((m - z.y) - z.x) + st.l2s) * kLn2);
+    // loss = T^2 sum_s q_s (log q_s + (lse - z_s)); lse - z_s in units of log2 is
+    // (m - n) - (z - n) + log2(sum), which keeps the digits of a small loss.
+    st.l2s = log2f(s);
+    const int64_t at = static_cast<int64_t>(row) * p.k;
+    any = p.sidx[at] != kNoTarget;
+    for (int j = a; j < p.k; j += 32) {
+      if (p.sidx[at + j] == kNoTarget) break;
+      const float lq = p.logq[at + j], q = expf(lq);
+      const float2 z = p.ztgt[at + j];
+      if (q != 0.0f) total += q * (lq + (((m - z.y) - z.x) + st.l2s) * kLn2);
     }
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   }
-  for (int d = 16; d > 0; d >>= 1) part_loss += __shfl_xor_sync(0xffffffffu, part_loss, d);
-  const float g = any ? (dloss ? dloss[row] : 1.0f) * temp : 0.0f;
+  const float g = any ? (p.dloss ? p.dloss[row] : 1.0f) * p.temp : 0.0f;
   if (a == 0) {
-    loss[row] = any ? part_loss * (temp * temp) : 0.0f;
-    lse[row] = (m + st.l2s) * kLn2;
-    if (e) {
-      stat[row] = st;
-      // cross entropy: p - 1 = expm1(-loss) at the label
-      const float d = labels && any ? expm1f(-part_loss) * g : 0.0f;
-      rscale[row] = make_float4(exp2f(-((m - st.r) + st.l2s)), g, d,
-                                __int_as_float(labels && any ? static_cast<int>(labels[row]) : -1));
+    p.loss[row] = any ? total * (p.temp * p.temp) : 0.0f;
+    p.lse[row] = (st.m + st.l2s) * kLn2;
+    if (p.e) {
+      p.stat[row] = st;
+      p.rscale[row] = make_float4(exp2f(-((st.m - st.r) + st.l2s)), g, d * g, __int_as_float(label));
     }
   }
-  if (e && g != 0.0f && !big)
-    write_targets(e + row * lde, st, a, labels, row, sidx, logq, k, ztgt);
+  if (p.e && !p.labels && g != 0.0f && !big)
+    write_targets(p.e + row * p.lde, st, a, row, p.sidx, p.logq, p.k, p.ztgt);
 }
 
 __device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
@@ -731,13 +774,13 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
 }
 
 // Brings the rows that hold a segment with its own reference to the row's common
-// one, then writes their target columns.  A block takes every gridDim.x-th row;
+// one, then writes their teacher's columns.  A block takes every gridDim.x-th row;
 // usually no row is marked, which its threads see in one look at 256 of them.
 __global__ void __launch_bounds__(256)
     k_head_rescale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int tn, int sw, int nseg,
                    int rows, const RowStat* __restrict__ stat, const float4* __restrict__ rscale,
-                   const int64_t* __restrict__ labels, const int* __restrict__ sidx, const float* __restrict__ logq,
-                   int k, const float2* __restrict__ ztgt) {
+                   const int* __restrict__ sidx, const float* __restrict__ logq, int k,
+                   const float2* __restrict__ ztgt) {
   pdl_trigger();
   pdl_wait();
   const int chunks = static_cast<int>(lde / 8), per_tile = tn / 8, per_seg = sw / 8;
@@ -765,8 +808,7 @@ __global__ void __launch_bounds__(256)
       v[c] = x;
     }
     __syncthreads();
-    if (threadIdx.x < 32) write_targets(er, st, threadIdx.x, labels, row, sidx, logq, k, ztgt);
-    __syncthreads();
+    if (sidx && threadIdx.x < 32) write_targets(er, st, threadIdx.x, row, sidx, logq, k, ztgt);
   }
 }
 
@@ -1072,18 +1114,36 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     if (few) err = launch_few_logits(h, X, seg.sw, p, st);
     else err = launch_pairs<0, 1>(ma, mb, me, a.K, g, p, st);
     if (err != cudaSuccess) return err;
+    StatArgs t{};
+    t.part = s.part;
+    t.nseg = seg.count;
+    t.rows = p.rows;
+    t.N = p.cols;
+    t.K = static_cast<int>(a.K);
+    t.labels = p.labels;
+    t.X = few ? nullptr : X;
+    t.W = W;
+    t.sidx = s.sidx;
+    t.logq = s.logq;
+    t.k = a.k;
+    t.ztgt = s.ztgt;
+    t.c = p.c;
+    t.temp = a.temperature;
+    t.dloss = a.dloss ? a.dloss + r0 : nullptr;
+    t.loss = a.loss + r0;
+    t.lse = a.lse + r0;
+    t.stat = s.stat;
+    t.rscale = s.rscale;
+    t.e = s.e;
+    t.lde = lde;
     err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
-                    true,
-                    static_cast<const float2*>(s.part), seg.count, p.rows, p.cols, p.labels,
-                    static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
-                    static_cast<const float2*>(s.ztgt), a.temperature, a.dloss ? a.dloss + r0 : nullptr, a.loss + r0,
-                    a.lse + r0, s.stat, s.rscale, s.e, lde);
+                    true, t);
     if (err != cudaSuccess) return err;
     if (!grad) continue;
     err = launch_ex(k_head_rescale, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 4 * device_sm_count()))),
                     dim3(256), 0, st, true, s.e, lde, static_cast<const float2*>(s.part), seg.tn, seg.sw, seg.count,
-                    p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float4*>(s.rscale), p.labels,
-                    static_cast<const int*>(s.sidx), static_cast<const float*>(s.logq), a.k,
+                    p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float4*>(s.rscale), static_cast<const int*>(s.sidx),
+                     static_cast<const float*>(s.logq), a.k,
                     static_cast<const float2*>(s.ztgt));
     if (err != cudaSuccess) return err;
     HeadEpi q{};

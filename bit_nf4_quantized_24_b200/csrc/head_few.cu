@@ -268,15 +268,27 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
           // The warp's four tokens together: each step is a chain of shuffles.
           constexpr int TW = BUF_TOKENS / 4;
           const int j0 = ew * TW, c0 = 4 * lane;
-          float e[TW][4], ref[TW], sum[TW], mx[TW];
+          float e[TW][4], ref[TW], sum[TW], mx[TW], zy[TW];
+          int label[TW];  // the token's label in this tile (its logit: zy), or -1
+#pragma unroll
+          for (int u = 0; u < TW; ++u) {
+            label[u] = -1;
+            if (p.labels && m + j0 + u < tokens) {
+              const int64_t y = p.labels[m + j0 + u] - v0;
+              if (y >= 0 && y < ncols) label[u] = static_cast<int>(y);
+            }
+          }
 #pragma unroll
           for (int u = 0; u < TW; ++u) {
             const float4 x = *reinterpret_cast<const float4*>(bp + (j0 + u) * BUF_PITCH + c0);
             e[u][0] = x.x, e[u][1] = x.y, e[u][2] = x.z, e[u][3] = x.w;
             mx[u] = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (c0 + q < ncols) mx[u] = fmaxf(mx[u], e[u][q]);
+            for (int q = 0; q < 4; ++q) {
+              if (c0 + q == label[u]) zy[u] = e[u][q];
+              if (c0 + q >= ncols || c0 + q == label[u]) e[u][q] = -INFINITY;  // a label stays out of the sums
+              mx[u] = fmaxf(mx[u], e[u][q]);
+            }
           }
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1)
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
           for (int u = 0; u < TW; ++u) {
             ref[u] = mx[u] == -INFINITY ? 0.0f : rintf(mx[u] * p.c);  // as in head.cu
 #pragma unroll
-            for (int q = 0; q < 4; ++q) e[u][q] = c0 + q < ncols ? exp2_fast(fmaf(e[u][q], p.c, -ref[u])) : 0.0f;
+            for (int q = 0; q < 4; ++q) e[u][q] = exp2_fast(fmaf(e[u][q], p.c, -ref[u]));
             sum[u] = (e[u][0] + e[u][1]) + (e[u][2] + e[u][3]);
           }
 #pragma unroll
@@ -310,9 +322,10 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
                   *reinterpret_cast<uint2*>(er + (c - v0)) = make_uint2(0u, 0u);
             }
             if (p.labels) {
-              const int64_t y = p.labels[row];
-              if (lane == 0 && y >= v0 && y < v0 + ncols)
-                p.ztgt[row] = make_float2(fmaf(bp[j * BUF_PITCH + static_cast<int>(y - v0)], p.c, -ref[u]), ref[u]);
+              if (label[u] >= 0 && label[u] / 4 == lane) {
+                const float n = rintf(zy[u] * p.c);
+                p.ztgt[row] = make_float2(fmaf(zy[u], p.c, -n), n);
+              }
             } else {
               const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.tiles + 1) + nt;
               for (int s = o[0] + lane; s < o[1]; s += 32) {
@@ -505,8 +518,9 @@ FewGrid few_grid(int64_t tokens, int parts) {
   FewGrid g{};
   g.tp = static_cast<int>((tokens + 15) / 16 * 16);
   g.stages = few_stages(g.tp);
-  // As many accumulators as the contraction has thousands, while two sets fit
-  // TMEM (see CHUNK in head.cu).
+  // A logit's contraction fills several accumulators in turn, which the epilogue
+  // adds up: as many as two sets of fit TMEM, each for at least 256 of it (the
+  // tensor core's additions truncate, see CHUNK in head.cu).
   g.parts = std::max(1, std::min(parts, 256 / g.tp));
   g.cols = 32;
   while (g.cols < 2 * g.parts * g.tp) g.cols *= 2;
@@ -574,7 +588,7 @@ int few_splits(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, static_cast<int>((h.K + 1023) / 1024));
+  FewGrid g = few_grid(p.rows, static_cast<int>((h.K + 255) / 256));
   g.br = br;
   g.tiles = static_cast<int>((h.N + br - 1) / br);
   g.nsplit = 1;

@@ -215,7 +215,6 @@ def test_distill_of_one_slot_is_cross_entropy(L):
     dloss = torch.rand(M, generator=g).cuda()
     a = qb.qlora_head_xent(head, X, labels, dloss=dloss)
     b = qb.qlora_head_distill(head, X, labels[:, None].contiguous(), torch.zeros(M, 1, device="cuda"), 1.0, dloss=dloss)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)  # (the distillation rounds its p - q to bf16)
     compare(a, ref)
     compare(b, ref)
@@ -241,7 +240,8 @@ def test_left_out_and_broken_rows(L):
     rest = [i for i in range(M) if i not in (4, 5, 6)]
     assert all(torch.equal(a[rest], b[rest]) for a, b in zip(good, (loss, lse, dx)))
     loss, lse, dx = qb.qlora_head_xent(head, X, torch.full_like(labels, -100), dloss=dloss)
-    assert (loss == 0).all() and (dx == 0).all() and torch.equal(lse, good[1])
+    assert (loss == 0).all() and (dx == 0).all()
+    compare((loss, lse, None), reference(values, X, 1.0, *xent_targets(torch.full_like(labels, -100), N), None))
     idx, t = teacher(g, M, N, 5, False, empty=False)
     t[8, 2], idx[9] = math.nan, -1
     loss, _, dx = qb.qlora_head_distill(head, X, idx, t, 1.0, dloss=dloss)
@@ -252,10 +252,9 @@ def test_left_out_and_broken_rows(L):
 
 @gpu
 def test_confident_tokens_keep_the_digits_of_their_gradient(L):
-    """A label with p near 1: loss and p - 1 are small differences, held to their own size.  The sum of exponentials
-    is 1 + loss; the label's 1 passes 5 additions in its group of 32, 8 in its tile, 1 + 5 over the tiles and lanes,
-    then log2, two products with ln 2 and expm1: 24 fp32 roundings near 1.  The entries of p - q are rounded to bf16
-    once and dX once, the row's factors three times in fp32."""
+    """A label with p near 1: loss and p - 1 are small differences, held to their own size.  The loss is log1p of the
+    others' sum over the label's exponential, so its relative error is that of the exponent: D and the fp32 steps of
+    reference() times 2, and 64 roundings.  p - 1 is rounded in fp32 alone, e to bf16 once and dX once."""
     M, N, K = 64, 500, 256
     g = wl.generator(3)
     W = torch.randn(N, K, generator=g).sign() * 0.125
@@ -268,7 +267,8 @@ def test_confident_tokens_keep_the_digits_of_their_gradient(L):
     compare(got, ref)
     rel = (got[2].double() - ref["dx"]).norm(dim=1) / ref["dx"].norm(dim=1)
     assert ref["loss"].min() < 1e-6
-    assert (rel <= 24 * U / ref["loss"] + 3 * B16)[ref["loss"] > 1e-5].all()
+    assert (rel <= 2 * ref["tol_loss"] + 64 * U + 3 * B16).all()
+    assert ((got[0] - ref["loss"]).abs() <= (2 * ref["tol_loss"] + 64 * U) * ref["loss"]).all()
 
 
 @gpu
