@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       if (!wait_warp(empty(r.slot), r.phase ^ 1, abort, status)) break;
       advance(w, groups);
       expand(0, a);
-      fetch(w, 0, a);
       expand(1, b);
+      fetch(w, 0, a);  // after both: the second expansion would wait for these loads too
       fetch(w, 1, b);
       fence_proxy_async_smem();
       __syncwarp();
@@ -519,7 +519,7 @@ FewGrid few_grid(int64_t tokens, int parts) {
   g.tp = static_cast<int>((tokens + 15) / 16 * 16);
   g.stages = few_stages(g.tp);
   // A logit's contraction fills several accumulators in turn, which the epilogue
-  // adds up: as many as two sets of fit TMEM, each for at least 256 of it (the
+  // adds up: up to 8, while two sets fit TMEM, each for at least 256 of it (the
   // tensor core's additions truncate, see CHUNK in head.cu).
   g.parts = std::max(1, std::min(parts, 256 / g.tp));
   g.cols = 32;
@@ -588,7 +588,7 @@ int few_splits(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, static_cast<int>((h.K + 255) / 256));
+  FewGrid g = few_grid(p.rows, static_cast<int>(std::min<int64_t>((h.K + 255) / 256, 8)));
   g.br = br;
   g.tiles = static_cast<int>((h.N + br - 1) / br);
   g.nsplit = 1;

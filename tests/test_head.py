@@ -169,8 +169,10 @@ def test_xent_nf4_head(L, block, dq, M, N, K):
     ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)
     got = qb.qlora_head_xent(head, X, labels, dloss=dloss)
     compare(got, ref)
-    same = qb.qlora_head_xent(values, X, labels, dloss=dloss)  # the bf16 values as a head: the same products
-    assert all(torch.equal(a, b) for a, b in zip(got, same))
+    same = qb.qlora_head_xent(values, X, labels, dloss=dloss)  # the bf16 values as a head
+    compare(same, ref)
+    if M <= 64 or M > 128:  # the same sums in the same order (between, the two heads' stages differ in length)
+        assert all(torch.equal(a, b) for a, b in zip(got, same))
 
 
 @gpu
