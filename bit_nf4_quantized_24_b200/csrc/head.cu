@@ -30,7 +30,7 @@
 //  - e needs no maximum subtracted as long as it fits the exponent of bf16, which
 //    is that of fp32: a segment whose maximum is within 2^-64 .. 2^64 is stored as
 //    it is.  A segment outside (a logit past 44) is stored relative to its own
-//    reference, and k_head_rescale then brings the rows that have one to a common
+//    reference, and k_head_stats then brings the rows that have one to a common
 //    reference, by exact powers of two.
 #include <algorithm>
 #include <atomic>
@@ -618,7 +618,6 @@ __device__ __forceinline__ float shift2(float x, float top) { return x == -INFIN
 // digits of z - lse.
 struct RowStat {
   float m, l2s, r;
-  int rescale;  // some segment is stored relative to its own reference
 };
 
 // Writes p - q, relative to reference r, into the columns of the row's teacher
@@ -661,11 +660,35 @@ struct StatArgs {
   float c, temp;
   const float* dloss;
   float *loss, *lse;
-  RowStat* stat;
   float4* rscale;
   uint16_t* e;  // null: no gradient
   int64_t lde;
+  int tn, sw;   // column segments of e (see Segments)
 };
+
+__device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
+  return bf16x2_bits(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+}
+
+// Brings a row that holds a segment with its own reference to the common one, r,
+// by powers of two (one warp; such rows are rare, and if all are, their warps
+// together are bound by HBM like any other pass).
+__device__ __noinline__ void rescale_row(const StatArgs& p, int row, float r, int lane) {
+  uint4* v = reinterpret_cast<uint4*>(p.e + row * p.lde);
+  const int n = static_cast<int>(p.lde / 8), per_tile = p.tn / 8, per_seg = p.sw / 8;
+  for (int c = lane; c < n; c += 32) {
+    const int q = c / per_tile, t = min(2 * q + (c - q * per_tile >= per_seg ? 1 : 0), p.nseg - 1);
+    const float ref = p.part[static_cast<int64_t>(t) * p.rows + row].x;
+    const float f = exp2f((fabsf(ref) <= kHeadFits ? 0.0f : ref) - r);
+    uint4 x = v[c];
+    x.x = scale_pair(x.x, f);
+    x.y = scale_pair(x.y, f);
+    x.z = scale_pair(x.z, f);
+    x.w = scale_pair(x.w, f);
+    v[c] = x;
+  }
+  __syncwarp();
+}
 
 // Joins the segments' (reference, sum) pairs of 8 rows per block: first thread
 // (r, j) takes row r and segments j, j + 64, ..., then warp r joins its row's 64
@@ -708,7 +731,7 @@ __global__ void __launch_bounds__(SROWS * SLANES) k_head_stats(const __grid_cons
   s = v.y * shift2(v.x, m) + w.y * shift2(w.x, m);
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   big = own[b] != 0;
-  RowStat st{m, 0.0f, big ? m : 0.0f, big ? 1 : 0};
+  RowStat st{m, 0.0f, big ? m : 0.0f};
   float total = 0.0f, d = 0.0f;  // the loss / T^2, and the label's p - 1
   bool any = false;
   int label = -1;
@@ -761,54 +784,12 @@ __global__ void __launch_bounds__(SROWS * SLANES) k_head_stats(const __grid_cons
     p.loss[row] = any ? total * (p.temp * p.temp) : 0.0f;
     p.lse[row] = (st.m + st.l2s) * kLn2;
     if (p.e) {
-      p.stat[row] = st;
       p.rscale[row] = make_float4(exp2f(-((st.m - st.r) + st.l2s)), g, d * g, __int_as_float(label));
     }
   }
-  if (p.e && !p.labels && g != 0.0f && !big)
-    write_targets(p.e + row * p.lde, st, a, row, p.sidx, p.logq, p.k, p.ztgt);
-}
-
-__device__ __forceinline__ uint32_t scale_pair(uint32_t v, float f) {
-  return bf16x2_bits(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
-}
-
-// Brings the rows that hold a segment with its own reference to the row's common
-// one, then writes their teacher's columns.  A block takes every gridDim.x-th row;
-// usually no row is marked, which its threads see in one look at 256 of them.
-__global__ void __launch_bounds__(256)
-    k_head_rescale(uint16_t* __restrict__ e, int64_t lde, const float2* __restrict__ part, int tn, int sw, int nseg,
-                   int rows, const RowStat* __restrict__ stat, const float4* __restrict__ rscale,
-                   const int* __restrict__ sidx, const float* __restrict__ logq, int k,
-                   const float2* __restrict__ ztgt) {
-  pdl_trigger();
-  pdl_wait();
-  const int chunks = static_cast<int>(lde / 8), per_tile = tn / 8, per_seg = sw / 8;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
-    if ((row - static_cast<int>(blockIdx.x)) % (256 * static_cast<int>(gridDim.x)) == 0) {
-      const int64_t mine = row + static_cast<int64_t>(threadIdx.x) * gridDim.x;
-      if (!__syncthreads_or(mine < rows && stat[mine].rescale)) {
-        row += 255 * gridDim.x;
-        continue;
-      }
-    }
-    const RowStat st = stat[row];
-    if (!st.rescale || rscale[row].y == 0.0f) continue;
-    uint16_t* er = e + static_cast<int64_t>(row) * lde;
-    uint4* v = reinterpret_cast<uint4*>(er);
-    for (int c = threadIdx.x; c < chunks; c += 256) {
-      const int q = c / per_tile, t = min(2 * q + (c - q * per_tile >= per_seg ? 1 : 0), nseg - 1);
-      const float n = part[static_cast<int64_t>(t) * rows + row].x;
-      const float f = exp2f((fabsf(n) <= kHeadFits ? 0.0f : n) - st.r);
-      uint4 x = v[c];
-      x.x = scale_pair(x.x, f);
-      x.y = scale_pair(x.y, f);
-      x.z = scale_pair(x.z, f);
-      x.w = scale_pair(x.w, f);
-      v[c] = x;
-    }
-    __syncthreads();
-    if (sidx && threadIdx.x < 32) write_targets(er, st, threadIdx.x, row, sidx, logq, k, ztgt);
+  if (p.e && g != 0.0f) {  // otherwise the row's gradient is written as zeros
+    if (big) rescale_row(p, row, st.r, a);
+    if (!p.labels) write_targets(p.e + row * p.lde, st, a, row, p.sidx, p.logq, p.k, p.ztgt);
   }
 }
 
@@ -979,7 +960,6 @@ struct HeadSpace {
   float2* part;
   float2* ztgt;
   float4* rscale;
-  RowStat* stat;
   float *logq, *split;
   int* sidx;
   uint16_t *off, *e;
@@ -1008,7 +988,6 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
     s.off = static_cast<uint16_t*>(take((std::max(segs, last_segs) + rows) * 2));
   }
   if (grad) {
-    s.stat = static_cast<RowStat*>(take(static_cast<size_t>(rows) * sizeof(RowStat)));
     s.rscale = static_cast<float4*>(take(static_cast<size_t>(rows) * 16));
     s.e = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * e_pitch(N) * 2));
     s.split = static_cast<float*>(take(std::max(split_bytes(rows, N, K), split_bytes(last, N, K))));
@@ -1132,20 +1111,15 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     t.dloss = a.dloss ? a.dloss + r0 : nullptr;
     t.loss = a.loss + r0;
     t.lse = a.lse + r0;
-    t.stat = s.stat;
     t.rscale = s.rscale;
     t.e = s.e;
     t.lde = lde;
+    t.tn = seg.tn;
+    t.sw = seg.sw;
     err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
                     true, t);
     if (err != cudaSuccess) return err;
     if (!grad) continue;
-    err = launch_ex(k_head_rescale, dim3(static_cast<unsigned>(std::min<int64_t>(rows, 4 * device_sm_count()))),
-                    dim3(256), 0, st, true, s.e, lde, static_cast<const float2*>(s.part), seg.tn, seg.sw, seg.count,
-                    p.rows, static_cast<const RowStat*>(s.stat), static_cast<const float4*>(s.rscale), static_cast<const int*>(s.sidx),
-                     static_cast<const float*>(s.logq), a.k,
-                    static_cast<const float2*>(s.ztgt));
-    if (err != cudaSuccess) return err;
     HeadEpi q{};
     q.rows = p.rows;
     q.cols = static_cast<int>(a.K);
