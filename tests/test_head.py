@@ -138,7 +138,8 @@ def teacher(g, M, N, k, bf16, empty=True):
 SHAPES = [
     (1, 1, 64), (1, 7, 64), (2, 256, 64), (3, 65, 128), (16, 257, 192), (127, 1000, 64), (128, 255, 512),
     (129, 511, 128), (256, 2048, 256), (257, 513, 64), (300, 2049, 320), (600, 4099, 576), (1, 32003, 1024),
-    (17, 9001, 2112), (100, 5000, 192), (128, 32003, 640), (40, 40001, 64), (90, 33333, 128),
+    (17, 9001, 2112), (60, 5000, 192), (64, 32003, 640), (40, 40001, 64), (65, 33333, 128),
+    (90, 33333, 128), (128, 32003, 640),
     (2290, 4090, 8192),  # tiles of 512 in both products
 ]
 
