@@ -487,6 +487,8 @@ def _head_call(fn, what, head, X, k, targets, scalars, dloss, outs, workspace, s
             _req(t, dtype, name, shape)
             tensors.append(t)
     if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         tensors.append(workspace)
     dev = X.device
     for t in tensors:

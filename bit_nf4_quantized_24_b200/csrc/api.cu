@@ -350,7 +350,7 @@ const char* qlora_status_string(int status) {
 
 int qlora_last_cuda_error(void) { return t_last_cuda_error; }
 
-int qlora_version(void) { return (1 << 16) | 0; }
+int qlora_version(void) { return (1 << 16) | 1; }
 
 int nf4_quantized_sizes(int64_t N, int64_t K, int block, int dq_block, size_t* codes_bytes, size_t* absmax_bytes,
                         size_t* dq_scale_bytes) {

@@ -142,7 +142,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int STAGE_BYTES = A_BYTES + NH * B_BYTES;
   constexpr int STAGES = RING_BYTES / STAGE_BYTES;
   static_assert(STAGES <= MAX_STAGES, "barrier block");
-  pdl_trigger();
+  // The last kernel of a call lets nothing start early: the layer's GEMM, launched
+  // early itself, reads its activations (this call's dX, say) without waiting for
+  // more than the kernel before it has begun.
+  if (MODE == 0 || g.ntail > 0) pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -528,7 +531,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Sum of the pieces of the split gradient tiles in piece order, times the row's
 // factor, rounded once to bf16.  Thread: 8 consecutive outputs of a row.
 __global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ split, HeadGrid g, HeadEpi p) {
-  pdl_trigger();
   pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int groups = g.tn / 8, per_tile = TM * groups;
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
   const int s = threadIdx.x;
   for (int j = s; j < k; j += blockDim.x) {
     const int64_t y = idx[row * k + j];
-    const float x = static_cast<float>(logit[row * k + j]) * inv_t;
+    const float x = static_cast<float>(logit[row * k + j]);
     const bool kept = y >= 0 && y < N && x != -INFINITY;
     key[j] = kept ? static_cast<int>(y) : kNoTarget;
     val[j] = x;
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
   for (int j = 0; j < k; ++j)
     if (key[j] != kNoTarget) mx = fmaxf(mx, val[j]);
   for (int j = 0; j < k; ++j)
-    if (key[j] != kNoTarget) sum += expf(val[j] - mx);
+    if (key[j] != kNoTarget) sum += expf((val[j] - mx) * inv_t);
   const float lsum = logf(sum);
   for (int j = s; j < k; j += blockDim.x) {
     const int mine = key[j];
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
     for (int o = 0; o < k; ++o) rank += (key[o] < mine || (key[o] == mine && o < j)) ? 1 : 0;
     sorted[rank] = mine;
     sidx[row * k + rank] = mine;
-    logq[row * k + rank] = mine == kNoTarget ? -INFINITY : (val[j] - mx) - lsum;
+    logq[row * k + rank] = mine == kNoTarget ? -INFINITY : (val[j] - mx) * inv_t - lsum;
   }
   __syncthreads();
   for (int t = s; t <= nseg; t += blockDim.x) {
@@ -699,7 +701,7 @@ __device__ __noinline__ void rescale_row(const StatArgs& p, int row, float r, in
 // 50003 x 2048 1.4e-6 off instead of 4e-7.
 constexpr int SROWS = 8, SLANES = 64;
 __global__ void __launch_bounds__(SROWS * SLANES) k_head_stats(const __grid_constant__ StatArgs p) {
-  pdl_trigger();
+  if (p.e) pdl_trigger();  // without a gradient this is the call's last kernel
   pdl_wait();
   __shared__ float2 sh[SROWS][SLANES + 1];
   __shared__ int own[SROWS];

@@ -181,7 +181,7 @@ def test_xent_nf4_head(L, block, dq, M, N, K):
 @pytest.mark.parametrize("M,N,K,k,T,bf16", [
     (1, 1, 64, 1, 1.0, False), (5, 300, 64, 1, 2.0, False), (9, 65, 128, 7, 1.5, True), (130, 1000, 192, 64, 2.0, False),
     (257, 513, 64, 33, 4.0, True), (300, 2049, 320, 256, 0.5, False), (64, 40, 64, 100, 1.0, False),
-    (520, 4099, 576, 128, 1.0, True),
+    (520, 4099, 576, 128, 1.0, True), (70, 3000, 128, 12, 1e-4, False), (200, 3000, 128, 12, 1e4, True),
 ])
 def test_distill(L, M, N, K, k, T, bf16, grad):
     head, values, X, _, g = make(M + N + K + k, M, N, K)
@@ -476,6 +476,38 @@ def test_training_step_of_a_layer_under_the_head(L, oracle):
         assert rel <= 1e-2, (name, rel)
 
 
+@gpu
+@pytest.mark.parametrize("M", [32, 1024])
+def test_chain_repeated_without_a_wait(L, M):
+    """Layer forward, head loss, layer backward enqueued twenty times on one stream with nothing in between, each
+    from other inputs: every kernel may be launched while the one before it still runs, and none may read what that
+    one has yet to write.  Each result is the one of the same calls with a synchronisation after every call."""
+    N, K, r, V = 1024, 512, 16, 3003
+    p = wl.draw_small(91, M, N, K, r, 2.0 * r, b_std=0.05)
+    q = qb.nf4_quantize(p["W"].cuda())
+    A, Bl = p["A"].cuda(), p["B"].cuda()
+    g = wl.generator(92)
+    head = (torch.randn(V, N, generator=g) * 0.05).bfloat16().cuda()
+    labels = torch.randint(0, V, (M,), generator=g).cuda()
+    dloss = torch.full((M,), 1.0 / M, device="cuda")
+    inputs = [torch.randn(M, K, generator=g).bfloat16().cuda() for _ in range(20)]
+
+    def chain(X, wait):
+        Y, H = qb.qlora_linear_fwd(q, X, A, Bl, p["scale"])
+        wait()
+        loss, lse, dY = qb.qlora_head_xent(head, Y, labels, dloss=dloss)
+        wait()
+        out = (loss, lse, dY, *qb.qlora_linear_bwd(q, X, dY, A, Bl, p["scale"], H=H))
+        wait()
+        return out
+
+    want = [chain(X, torch.cuda.synchronize) for X in inputs]
+    got = [chain(X, lambda: None) for X in inputs]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 # ------------------------------------------------------------ without a GPU
 
 
@@ -571,7 +603,8 @@ def test_binding_refusals_of_gpu_tensors(L):
     c = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
     W, X, y = c(10, 64), c(3, 64), c(3, dt=torch.int64)
     for bad in (dict(X=c(3, 128)), dict(X=c(3)), dict(labels=c(4, dt=torch.int64)), dict(dloss=c(4, dt=torch.float32)),
-                dict(X=c(64, 3).t()), dict(head=c(64)), dict(outs=(None, None, X.clone()))):
+                dict(X=c(64, 3).t()), dict(head=c(64)), dict(outs=(None, None, X.clone())),
+                dict(workspace=c(1 << 20, 2, dt=torch.uint8)[:, 0]), dict(labels=torch.zeros(3, dtype=torch.int64))):
         with pytest.raises(ValueError):
             qb.qlora_head_xent(**{**dict(head=W, X=X, labels=y), **bad})
     for bad in (dict(labels=y.int()), dict(X=X.float()), dict(head=W.half()), dict(dloss=c(3))):
