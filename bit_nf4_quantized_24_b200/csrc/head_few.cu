@@ -375,15 +375,18 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       uint32_t c[8];
       uint32_t q0, q1;
       float s0, s1;
-      bool valid;
+      bool valid, zero;  // has weights; must hold zeros
     };
     auto fetch = [&](const Walk& w, int u, Part& f) {
-      f.valid = false;
+      f.valid = f.zero = false;
       if (w.i >= nitems) return;
       const int at0 = (w.k * SUB + u) * BK;
       const int wrow = MODE == 0 ? w.nt * g.br + t : at0 + (t & 63);
       const int kcol = MODE == 0 ? at0 : w.nt * UM + 64 * (t >> 6);
-      if (wrow >= N || kcol >= K || (MODE == 0 && t >= g.br)) return;
+      // Past the end of the contraction the token tile is zero, and the head must be
+      // finite; MMA rows without an output may hold anything.
+      f.zero = at0 + (MODE == 0 ? 0 : t & 63) >= (MODE == 0 ? K : N);
+      if (f.zero || wrow >= N || kcol >= K || (MODE == 0 && t >= g.br)) return;
       f.valid = true;
       const int64_t at = static_cast<int64_t>(wrow) * K + kcol;
       ldg_nc_v8(codes + at / 2, f.c);
@@ -428,9 +431,9 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
             st_shared_v4(row_s + ((j ^ sw) << 4), o0, o1, o2, o3);
           }
         }
-      } else {
+      } else if (f.zero) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) st_shared_v4(row_s + (j << 4), 0u, 0u, 0u, 0u);
+        for (int j = 0; j < 8; ++j) st_shared_v4(row_s + ((j ^ sw) << 4), 0u, 0u, 0u, 0u);
       }
     };
     static_assert(SUB == 2, "one set of registers per sub-stage");
@@ -446,12 +449,12 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       advance(w, groups);
       expand(0, a);
       expand(1, b);
-      fetch(w, 0, a);  // after both: the second expansion would wait for these loads too
-      fetch(w, 1, b);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(r.slot));
       r.advance(groups, g.stages);
+      fetch(w, 0, a);  // after both: the second expansion would wait for these loads too
+      fetch(w, 1, b);
     }
   }
 
