@@ -348,10 +348,12 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
     // parity cannot tell the two turns apart.
     const int groups = min(DQ_GROUPS, g.stages);
     const int e = warp - 6, grp = e >> 2;
-    const int t = (e & 3) * 32 + lane;  // row of the 128-byte rows of the stage
-    const int KB = K / 64;
-    // Which (row, 64-weight group) of W this thread expands: MODE 0, row t of the
-    // tile; MODE 1, row t % 64 of the stage, columns 64 (t / 64) of the tile.
+    // A stage is 128 rows of W (MODE 0: of the tile; MODE 1: of the contraction) by
+    // two groups of 64 columns.  A thread expands one group of two rows, 16 apart,
+    // its neighbour the other group: their codes are 64 contiguous bytes, and a load
+    // touches 16 rows (a load instruction costs a cycle per 128-byte line; 16 tokens
+    // on a 32000 x 4096 head with the gradient: 108 us, with a row per lane 117).
+    const int row0 = (e & 3) * 32 + (lane >> 1), half = lane & 1;
     struct Walk {
       int i, nt, z, k, kend;
     };
@@ -367,26 +369,24 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
         w.k += over;
       }
     };
-    // The codes go from global memory to registers (32 bytes per thread and
-    // sub-stage: a whole sector), one of the group's stages ahead, with the one or
-    // two scales of their blocks.  Each sub-stage has its own registers: handing
-    // them on by moves would wait for the loads.
+    // The codes go from global memory to registers (32 bytes: a whole sector), one of
+    // the group's stages ahead, with the one or two scales of their blocks.  Each row
+    // has its own registers: handing them on by moves would wait for the loads.
     struct Part {
       uint32_t c[8];
       uint32_t q0, q1;
       float s0, s1;
       bool valid, zero;  // has weights; must hold zeros
     };
-    auto fetch = [&](const Walk& w, int u, Part& f) {
+    auto fetch = [&](const Walk& w, int row, Part& f) {
       f.valid = f.zero = false;
       if (w.i >= nitems) return;
-      const int at0 = (w.k * SUB + u) * BK;
-      const int wrow = MODE == 0 ? w.nt * g.br + t : at0 + (t & 63);
-      const int kcol = MODE == 0 ? at0 : w.nt * UM + 64 * (t >> 6);
+      const int wrow = MODE == 0 ? w.nt * g.br + row : w.k * (SUB * BK) + row;
+      const int kcol = MODE == 0 ? (w.k * SUB + half) * BK : w.nt * UM + 64 * half;
       // Past the end of the contraction the token tile is zero, and the head must be
       // finite; MMA rows without an output may hold anything.
-      f.zero = at0 + (MODE == 0 ? 0 : t & 63) >= (MODE == 0 ? K : N);
-      if (f.zero || wrow >= N || kcol >= K || (MODE == 0 && t >= g.br)) return;
+      f.zero = MODE == 0 ? kcol >= K : wrow >= N;
+      if (wrow >= N || kcol >= K || (MODE == 0 && row >= g.br)) return;
       f.valid = true;
       const int64_t at = static_cast<int64_t>(wrow) * K + kcol;
       ldg_nc_v8(codes + at / 2, f.c);
@@ -409,14 +409,24 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       }
     };
     RingPos r;
-    auto expand = [&](int u, const Part& f) {
-      const uint32_t row_s = base + r.slot * stage_bytes + u * W_BYTES + t * 128;
-      const uint32_t sw = t & 7;
+    auto expand = [&](int row, Part& f) {
+      const uint32_t row_s = base + r.slot * stage_bytes +
+                             (MODE == 0 ? half * W_BYTES + row * 128
+                                        : (row >> 6) * W_BYTES + half * 8192 + (row & 63) * 128);
+      // Neighbours write the same row of two tiles, so the same banks: the second one
+      // starts with its other four chunks.
+      const uint32_t sw = (row & 7) ^ (half << 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = f.c[j], y = f.c[j + 4];
+        f.c[j] = half ? y : x;
+        f.c[j + 4] = half ? x : y;
+      }
       if (f.valid) {
         const float a0 = (GEN && !dq) ? f.s0 : __fmul_rn(static_cast<float>(f.q0), f.s0);
-        const Nf4Lut lut = make_lut(lv, a0);
         if (GEN && lg == 5) {
-          const Nf4Lut lut1 = make_lut(lv, dq ? __fmul_rn(static_cast<float>(f.q1), f.s1) : f.s1);
+          const float a1 = dq ? __fmul_rn(static_cast<float>(f.q1), f.s1) : f.s1;
+          const Nf4Lut lut = make_lut(lv, half ? a1 : a0), lut1 = make_lut(lv, half ? a0 : a1);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint32_t o0, o1, o2, o3;
@@ -424,6 +434,7 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
             st_shared_v4(row_s + ((j ^ sw) << 4), o0, o1, o2, o3);
           }
         } else {
+          const Nf4Lut lut = make_lut(lv, a0);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint32_t o0, o1, o2, o3;
@@ -436,25 +447,25 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
         for (int j = 0; j < 8; ++j) st_shared_v4(row_s + ((j ^ sw) << 4), 0u, 0u, 0u, 0u);
       }
     };
-    static_assert(SUB == 2, "one set of registers per sub-stage");
+    static_assert(SUB == 2, "two groups of 64 columns, or two sets of 64 rows, per stage");
     Walk w{grp < groups ? static_cast<int>(blockIdx.x) : nitems, 0, 0, 0, 0};
     start(w);
     advance(w, grp);
     r.advance(grp, g.stages);
     Part a, b;
-    fetch(w, 0, a);
-    fetch(w, 1, b);
+    fetch(w, row0, a);
+    fetch(w, row0 + 16, b);
     while (w.i < nitems) {
       if (!wait_warp(empty(r.slot), r.phase ^ 1, abort, status)) break;
       advance(w, groups);
-      expand(0, a);
-      expand(1, b);
+      expand(row0, a);
+      expand(row0 + 16, b);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(r.slot));
       r.advance(groups, g.stages);
-      fetch(w, 0, a);  // after both: the second expansion would wait for these loads too
-      fetch(w, 1, b);
+      fetch(w, row0, a);  // after both: the second expansion would wait for these loads too
+      fetch(w, row0 + 16, b);
     }
   }
 
