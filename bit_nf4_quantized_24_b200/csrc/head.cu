@@ -463,35 +463,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (live)
           p.part[(2 * static_cast<int64_t>(nt) + h) * p.rows + row] = make_float2(mx == -INFINITY ? mx : ref, sum);
       } else {
+        const float4 f = live && tail < 0 ? p.rscale[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int label = live && tail < 0 ? __float_as_int(f.w) : -1;
+        const int width = min(cwidth, p.cols - n0);  // a multiple of 64, as both are; may be negative
+        const uint16_t* wl = label >= 0 ? p.W + static_cast<int64_t>(label) * p.cols + n0 : nullptr;
+        // The label's row of W, 64 columns at a time and 64 ahead of their use (the
+        // first before the accumulator is complete): a row per lane takes a
+        // microsecond to come.
+        auto fetch = [&](int col, uint4 (&w)[8]) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            w[q] = wl && col < width ? ldg_nc_v4(wl + col + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint4 w0[8], w1[8];
+        fetch(0, w0);
+        fetch(64, w1);
         if (!(ok = take(a))) break;
         const uint32_t acc = tmem + lane_base + (NH == 1 ? 256u * a + cseg : 256u * h);
-        if (used) {
-          const float4 f = live && tail < 0 ? p.rscale[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          const int label = live && tail < 0 ? __float_as_int(f.w) : -1;
-          const uint16_t* wl = label >= 0 ? p.W + static_cast<int64_t>(label) * p.cols + n0 : nullptr;
-#pragma unroll 1
-          for (int col = 0; col < cwidth && n0 + col < p.cols; col += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(acc + col, v);
-            uint4 w[4] = {};  // the label's row of W
-            if (wl) {
+        auto emit = [&](int col, const uint4 (&w)[8]) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) w[q] = ldg_nc_v4(wl + col + 8 * q);
-            }
+          for (int part = 0; part < 2; ++part) {
+            const int at = col + 32 * part;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc + at, v);
             tmem_ld_wait();
             if (tail >= 0) {  // a piece of a split tile: fp32 sums, joined by k_head_join
               float4* dst = reinterpret_cast<float4*>(
                   p.split + ((static_cast<int64_t>(tail) * g.nsplit + zp) * TM + rank * UM + quad * 32 + lane) * g.tn +
-                  cseg + col);
+                  cseg + at);
 #pragma unroll
               for (int q = 0; q < 8; ++q)
                 dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
                                      __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
             } else if (live) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n0 + col);
+              uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * p.cols + n0 + at);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {  // cols % 64 == 0: a group of 32 columns is whole
-                const uint32_t wq[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+              for (int q = 0; q < 4; ++q) {
+                const uint4 x = w[4 * part + q];
+                const uint32_t wq[4] = {x.x, x.y, x.z, x.w};
                 uint32_t o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -499,6 +508,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 dst[q] = make_uint4(o[0], o[1], o[2], o[3]);
               }
             }
+          }
+        };
+        if (used) {
+#pragma unroll 1
+          for (int col = 0; col < width; col += 128) {
+            emit(col, w0);
+            fetch(col + 128, w0);
+            if (col + 64 < width) emit(col + 64, w1);
+            fetch(col + 192, w1);
           }
         }
         give(a);

@@ -366,8 +366,8 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  * over c tokens: 1 / c), or NULL for ones; without dX it must be NULL.  Where
  * dloss[m] is 0 the row of dX is 0.  A NaN or an infinity among a token's
  * logits makes that token's lse, loss and dX NaN; other tokens are untouched.
- * Logits, statistics and sums are fp32; p - q is rounded to bf16 before the
- * second product and dX once more at the end.  Outputs must not overlap inputs.
+ * Logits, statistics and sums are fp32; p is rounded to bf16 before the second
+ * product (a label's and a token's largest p - q are not) and dX at the end.  Outputs must not overlap inputs.
  *
  * workspace: qlora_head_workspace bytes, 256-byte aligned.  Tokens are taken
  * in pieces; with a gradient the workspace holds M' x N bf16 values for a piece

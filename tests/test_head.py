@@ -12,7 +12,8 @@ Tolerances.  u = 2^-24 is the fp32 rounding, b = 2^-8 the bf16 one.
    64 roundings of terms no larger than |z| + |lse| + 1, plus 72 relative
    roundings of a sum of positive terms; the tolerance allows 160 u of that.
  - p is rounded once to bf16 (as e), and so is a teacher's p - q (a label's p - 1
-   stays in fp32); both carry the
+   and a row's
+   largest p - q stay in fp32); both carry the
    logits' 2 D and the fp32 steps of the exponent.  Entries of e below 2^-126 are
    flushed to 0, and e is stored relative to a reference that is at most 2^64
    above the row's sum (or factors of at least 2^-149 bring a value of at most
