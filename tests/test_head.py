@@ -12,18 +12,17 @@ Tolerances.  u = 2^-24 is the fp32 rounding, b = 2^-8 the bf16 one.
    64 roundings of terms no larger than |z| + |lse| + 1, plus 72 relative
    roundings of a sum of positive terms; the tolerance allows 160 u of that.
  - p is rounded once to bf16 (as e), and so is a teacher's p - q (a label's p - 1
-   and a row's
-   largest p - q stay in fp32); both carry the
-   logits' 2 D and the fp32 steps of the exponent.  Entries of e below 2^-126 are
-   flushed to 0, and e is stored relative to a reference that is at most 2^64
-   above the row's sum (or factors of at least 2^-149 bring a value of at most
-   2^64 to one that is), so an entry of p loses at most 2^-62 by that.  The second product adds fp32 steps over the vocabulary (N / 16 +
-   16 truncations, and the pieces of a split tile), and dX is rounded once.
+   and a row's largest p - q stay in fp32); both carry the logits' 2 D and the
+   fp32 steps of the exponent.  Entries of e below 2^-126 are flushed to 0, and e
+   is stored relative to a reference that is at most 2^64 above the row's sum (or
+   factors of at least 2^-149 bring a value of at most 2^64 to one that is), so an
+   entry of p loses at most 2^-62 by that.  The second product adds fp32 steps over
+   the vocabulary (N / 16 + 16 truncations, and the pieces of a split tile), and dX
+   is rounded once.
 """
 import ctypes
 import math
 
-import numpy as np
 import pytest
 import torch
 
@@ -331,6 +330,32 @@ def test_pieces_of_tokens(L, piece):
         got = qb.qlora_head_distill(head, a[0], a[1], a[2], 2.0, dloss=a[3], workspace=ws[:nbytes])
         compare(got, reference(values, a[0], 2.0, *distill_targets(a[1], a[2], N, 2.0), a[3]))
         assert (ws[nbytes:] == 171).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,N,grad", [(5000, 131072, True), (20000, 300, False)])
+def test_several_pieces_of_the_librarys_choice(L, M, N, grad):
+    """More tokens than the default workspace takes at once, with a gradient and without."""
+    K = 64
+    head, values, X, labels, g = make(M, M, N, K)
+    dloss = torch.rand(M, generator=g).cuda() if grad else None
+    got = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    compare(got, reference(values, X, 1.0, *xent_targets(labels, N), dloss))
+
+
+@gpu
+@pytest.mark.parametrize("M", [20, 300])
+def test_gradient_without_weights_is_that_of_the_sum(L, M):
+    """The C call with dX and a NULL dloss: weights of one."""
+    N, K = 700, 128
+    head, values, X, labels, g = make(M, M, N, K)
+    want = qb.qlora_head_xent(head, X, labels, dloss=torch.ones(M, device="cuda"))
+    loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    dX = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(qb.head_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+    assert L.qlora_head_xent(qb._ptr(head), None, None, None, 64, 256, N, K, qb._ptr(X), M, qb._ptr(labels), None,
+                             qb._ptr(loss), qb._ptr(lse), qb._ptr(dX), qb._ptr(ws), ws.numel(), qb._stream()) == 0
+    assert all(torch.equal(a, b) for a, b in zip((loss, lse, dX), want))
 
 
 @gpu
