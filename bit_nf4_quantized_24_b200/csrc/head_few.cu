@@ -26,9 +26,15 @@ constexpr int MAX_STAGES = 6;
 constexpr int DQ_GROUPS = 4;          // groups of 4 warps that take turns at expanding the stages
 constexpr int BUF_PITCH = UM + 4;     // floats per token in the epilogue's buffer
 constexpr int BUF_TOKENS = 16;
-constexpr int BUF_BYTES = 2 * BUF_TOKENS * BUF_PITCH * 4;
+constexpr int BUF_BYTES = 2 * BUF_TOKENS * BUF_PITCH * 4;  // per set of epilogue warps
+// Sets of four epilogue warps, which take turns at 16 tokens: two on a bf16 head
+// (128 tokens, 8000 x 1024 / 32000 x 2048 with the gradient: 38 / 73 us with one set,
+// 32 / 66 us with two); an NF4 head's block has no threads to spare.
+__host__ __device__ constexpr int epi_sets(bool nf4) { return nf4 ? 1 : 2; }
 constexpr int BAR_BYTES = 512;
 constexpr int SMEM_MAX = 232448;
+
+__host__ __device__ constexpr int threads_of(bool nf4) { return 64 + epi_sets(nf4) * 128 + (nf4 ? DQ_GROUPS * 128 : 0); }
 
 struct FewBars {
   uint64_t full[MAX_STAGES];   // head tile and token tile landed (or were written)
@@ -51,17 +57,19 @@ struct FewGrid {
   int cols;    // TMEM columns
 };
 
-__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_barrier(int set) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");
+}
 // The same barrier; tells all 128 threads whether ok holds for every one of them.
-__device__ __forceinline__ bool epilogue_all(bool ok) {
+__device__ __forceinline__ bool epilogue_all(int set, bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.red.and.pred q, 1, 128, p;\n\t"
+      "barrier.red.and.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(ok ? 1u : 0u)
+      : "r"(ok ? 1u : 0u), "r"(1 + set)
       : "memory");
   return r != 0;
 }
@@ -70,12 +78,13 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 // quantization); 2: NF4 with 2^lg-weight blocks, double quantization if dq.
 //   warp 0       TMA producer
 //   warp 1       TMEM allocation, MMA issue
-//   warps 2-5    epilogue (two accumulators alternate)
+//   warps 2-9    KIND 0: epilogue in two sets of four (two accumulators alternate)
+//   warps 2-5    KIND > 0: epilogue
 //   warps 6-21   KIND > 0: expansion of the codes
 // Every wait is bounded; on expiry the kernel records kDevTimeout, drains what
 // it issued, frees TMEM and returns.
 template <int MODE, int KIND>
-__global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
+__global__ void __launch_bounds__(threads_of(KIND > 0), 1)
     k_few(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, FewGrid g, HeadEpi p,
           const uint8_t* __restrict__ codes, const uint8_t* __restrict__ absmax_q, const float* __restrict__ dq_scale, Nf4Levels lv, int N, int K, int lg,
           int dq, int* status) {
@@ -86,7 +95,8 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   const int x_tile = g.tp * BK * 2, stage_bytes = SUB * (W_BYTES + x_tile);
   const uint32_t buf = base + g.stages * stage_bytes;
-  const uint32_t bar0 = buf + BUF_BYTES;
+  constexpr int SETS = epi_sets(NF4);
+  const uint32_t bar0 = buf + SETS * BUF_BYTES;
   FewBars* bars = reinterpret_cast<FewBars*>(smem_raw + (bar0 - raw));
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(acc_full(a), 1);
-      mbar_init(acc_empty(a), 4);
+      mbar_init(acc_empty(a), 4 * SETS);
     }
     mbar_init(drain_bar, 1);
     bars->abort = 0;
@@ -219,23 +229,23 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
       wait_drain(drain_bar, 0);
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 2 + 4 * SETS) {
     // ------------------------------------------------------------- epilogue
-    const int quad = warp & 3, ew = warp - 2;
+    const int quad = warp & 3, ew = (warp - 2) & 3, set = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     int t = 0, filled = 0;
     for (int i = blockIdx.x; i < nitems; i += gridDim.x, ++t) {
       int nt, z, kbeg, kend;
       item(i, nt, z, kbeg, kend);
-      // the four warps leave together: they meet at barriers
-      if (!epilogue_all(wait_bounded(acc_full(t & 1), (t >> 1) & 1, abort, status))) break;
+      // a set's four warps leave together: they meet at barriers
+      if (!epilogue_all(set, wait_bounded(acc_full(t & 1), (t >> 1) & 1, abort, status))) break;
       tc_fence_after();
       const uint32_t acc = tmem + lane_base + (t & 1) * g.parts * g.tp;
       if (MODE == 1) {
         const int k = nt * UM + quad * 32 + lane;
         float* dst = p.split + static_cast<int64_t>(z) * tokens * p.cols + k;
 #pragma unroll 1
-        for (int m = 0; m < tokens; m += 16) {
+        for (int m = 16 * set; m < tokens; m += 16 * SETS) {
           uint32_t v[16];
           tmem_ld_x16(acc + m, v);
           tmem_ld_wait();
@@ -250,10 +260,10 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
         const int ncols = min(g.br, p.cols - v0);                 // entries of the tile
         const int ewidth = static_cast<int>(min(static_cast<int64_t>(g.br), p.lde - v0));
 #pragma unroll 1
-        for (int m = 0; m < tokens; m += BUF_TOKENS, ++filled) {
+        for (int m = BUF_TOKENS * set; m < tokens; m += BUF_TOKENS * SETS, ++filled) {
           // 16 tokens x 128 entries into shared memory, token by token; then a warp
           // has a token's entries side by side
-          const uint32_t b = buf + (filled & 1) * (BUF_BYTES / 2);
+          const uint32_t b = buf + set * BUF_BYTES + (filled & 1) * (BUF_BYTES / 2);
           float* bp = reinterpret_cast<float*>(smem_raw + (b - raw));
           for (int q = 0; q < g.parts; ++q) {
             uint32_t v[16];
@@ -264,7 +274,7 @@ __global__ void __launch_bounds__(KIND ? 192 + DQ_GROUPS * 128 : 192, 1)
             for (int j = 0; j < BUF_TOKENS; ++j)
               x[j * BUF_PITCH] = q == 0 ? __uint_as_float(v[j]) : x[j * BUF_PITCH] + __uint_as_float(v[j]);
           }
-          epilogue_barrier();
+          epilogue_barrier(set);
           // The warp's four tokens together: each step is a chain of shuffles.
           constexpr int TW = BUF_TOKENS / 4;
           const int j0 = ew * TW, c0 = 4 * lane;
@@ -519,18 +529,18 @@ __global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ spli
 }
 
 // Ring depth and shared memory for `tokens` tokens.
-int few_stages(int tp) {
-  const int room = SMEM_MAX - 1024 - BAR_BYTES - BUF_BYTES;
+int few_stages(int tp, bool nf4) {
+  const int room = SMEM_MAX - 1024 - BAR_BYTES - epi_sets(nf4) * BUF_BYTES;
   return std::min(MAX_STAGES, room / (SUB * (W_BYTES + tp * BK * 2)));
 }
-int few_smem(const FewGrid& g) {
-  return 1024 + g.stages * SUB * (W_BYTES + g.tp * BK * 2) + BUF_BYTES + BAR_BYTES;
+int few_smem(const FewGrid& g, bool nf4) {
+  return 1024 + g.stages * SUB * (W_BYTES + g.tp * BK * 2) + epi_sets(nf4) * BUF_BYTES + BAR_BYTES;
 }
 
-FewGrid few_grid(int64_t tokens, int parts) {
+FewGrid few_grid(int64_t tokens, int parts, bool nf4) {
   FewGrid g{};
   g.tp = static_cast<int>((tokens + 15) / 16 * 16);
-  g.stages = few_stages(g.tp);
+  g.stages = few_stages(g.tp, nf4);
   // A logit's contraction fills several accumulators in turn, which the epilogue
   // adds up: up to 8, while two sets fit TMEM, each for at least 256 of it (the
   // tensor core's additions truncate, see CHUNK in head.cu).
@@ -548,7 +558,7 @@ cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& x, const FewGri
   int lg = 0;
   while ((1 << lg) < h.block) ++lg;
   const int grid = std::min(g.tiles * g.nsplit, device_sm_count());
-  return launch_ex(k_few<MODE, KIND>, dim3(grid), dim3(KIND ? 192 + DQ_GROUPS * 128 : 192), few_smem(g), st,
+  return launch_ex(k_few<MODE, KIND>, dim3(grid), dim3(threads_of(KIND > 0)), few_smem(g, KIND > 0), st,
                    true, w, x, g, p, h.codes, h.absmax_q, h.dq_scale, host_codebook().levels, static_cast<int>(h.N),
                    static_cast<int>(h.K), lg, h.dq_block ? 1 : 0, device_status_ptr());
 }
@@ -601,7 +611,7 @@ int few_splits(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, static_cast<int>(std::min<int64_t>((h.K + 255) / 256, 8)));
+  FewGrid g = few_grid(p.rows, static_cast<int>(std::min<int64_t>((h.K + 255) / 256, 8)), !h.W);
   g.br = br;
   g.tiles = static_cast<int>((h.N + br - 1) / br);
   g.nsplit = 1;
@@ -614,7 +624,7 @@ cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, co
 
 cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp, int nsplit, const HeadEpi& p,
                             cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, 1);
+  FewGrid g = few_grid(p.rows, 1, !h.W);
   g.br = UM;
   g.tiles = static_cast<int>((h.K + UM - 1) / UM);
   g.nsplit = nsplit;
