@@ -439,7 +439,8 @@ def qlora_linear_fwd_noalloc(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: 
 
 def head_workspace_bytes(M, N, K, k=0, want_dx=True, nf4=False, piece=0) -> int:
     """Workspace bytes of qlora_head_xent (k = 0) or qlora_head_distill (k teacher
-    slots per token); piece: tokens taken at once (0: the library's choice)."""
+    slots per token); piece: most tokens taken at once, in multiples of 256 (0: the
+    library's choice)."""
     b = ctypes.c_size_t()
     _check(lib().qlora_head_workspace(M, N, K, k, int(want_dx), int(nf4), piece, ctypes.byref(b)),
            "qlora_head_workspace")

@@ -967,10 +967,27 @@ HeadGrid grad_tiles(int64_t rows, int64_t N, int64_t K, int nh, double* cost) {
   *cost = static_cast<double>(full) * static_cast<double>(numK) * stage + tail;
   return g;
 }
+// The cheaper width's tiles.  A call asks for them several times (the workspace's
+// layout and the launch), and finding them takes a microsecond or two: the last
+// answer is kept per host thread.
 HeadGrid grad_grid(int64_t rows, int64_t N, int64_t K) {
-  double one = 0.0, two = 0.0;
-  const HeadGrid a = grad_tiles(rows, N, K, 1, &one), b = grad_tiles(rows, N, K, 2, &two);
-  return two < one ? b : a;
+  struct Plan {
+    int64_t rows = -1, N = 0, K = 0;
+    int pairs = 0;
+    HeadGrid g{};
+  };
+  thread_local Plan last;
+  const int P = head_pairs();
+  if (last.rows != rows || last.N != N || last.K != K || last.pairs != P) {
+    double one = 0.0, two = 0.0;
+    const HeadGrid a = grad_tiles(rows, N, K, 1, &one), b = grad_tiles(rows, N, K, 2, &two);
+    last.g = two < one ? b : a;
+    last.rows = rows;
+    last.N = N;
+    last.K = K;
+    last.pairs = P;
+  }
+  return last.g;
 }
 
 // The column segments of a piece's statistics: the first of a tile's two has sw
@@ -1064,18 +1081,19 @@ cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, const CUten
 }
 }  // namespace
 
+// Pieces are the library's choice or a smaller number of whole tiles (all of M, if
+// that is less than one).
 size_t head_workspace_bytes(int64_t piece, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad,
                             bool nf4) {
-  const int64_t rows = piece > 0 ? std::min(piece, std::max<int64_t>(M, 1)) : default_piece(M, N, grad);
+  int64_t rows = default_piece(M, N, grad);
+  if (piece > 0) rows = std::min(rows, std::max<int64_t>(piece / TM * TM, TM));
   return std::max<size_t>(256, head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes);
 }
 
 int64_t head_piece(size_t bytes, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad, bool nf4) {
   int64_t rows = default_piece(M, N, grad);
-  while (head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes > bytes) {
-    if (rows <= TM) return 0;
-    rows = ((rows + 1) / 2 + TM - 1) / TM * TM;
-  }
+  while (rows > 0 && head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes > bytes)
+    rows = (rows - 1) / TM * TM;
   return rows;
 }
 

@@ -373,9 +373,9 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  * in pieces; with a gradient the workspace holds M' x N bf16 values for a piece
  * of M' tokens.  piece = 0 asks for the bytes of the library's own choice (at
  * most 1 GB of such values), another piece for at most that many tokens at
- * a time; the calls use the largest pieces that fit the workspace they get,
- * down to 256 tokens (or M, if fewer), below which they return
- * QLORA_ERR_WORKSPACE.  k = 0 asks for qlora_head_xent, k >= 1 for
+ * a time, in multiples of 256 (256 at least, or M, if fewer); the calls use the
+ * largest such pieces that fit the workspace they get, and return
+ * QLORA_ERR_WORKSPACE if none does.  k = 0 asks for qlora_head_xent, k >= 1 for
  * qlora_head_distill with k slots; want_dx: dX is not NULL; nf4: an NF4 head.
  * Results do not depend on other work of the device, and repeat bit for bit
  * with the same workspace size.

@@ -333,6 +333,22 @@ def test_pieces_of_tokens(L, piece):
 
 
 @gpu
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M", [1, 100, 128, 129, 256, 257, 640, 900])
+def test_every_piece_that_can_be_asked_for(L, M, nf4):
+    """A workspace of any piece is enough for its call, also where fewer tokens need more of it for partial sums."""
+    N, K = 300, 1024
+    head, values, X, labels, g = make(M, M, N, K, 64 if nf4 else 0)
+    dloss = torch.rand(M, generator=g).cuda()
+    ref = reference(values, X, 1.0, *xent_targets(labels, N), dloss)
+    for piece in (1, 100, 256, 300, 512, 700, 0):
+        nbytes = qb.head_workspace_bytes(M, N, K, nf4=nf4, piece=piece)
+        ws = torch.full((nbytes + 4096,), 171, dtype=torch.uint8, device="cuda")
+        compare(qb.qlora_head_xent(head, X, labels, dloss=dloss, workspace=ws[:nbytes]), ref)
+        assert (ws[nbytes:] == 171).all()
+
+
+@gpu
 @pytest.mark.parametrize("M,N,grad", [(5000, 131072, True), (20000, 300, False)])
 def test_several_pieces_of_the_librarys_choice(L, M, N, grad):
     """More tokens than the default workspace takes at once, with a gradient and without."""
@@ -566,6 +582,10 @@ def test_workspace_sizes(L):
     assert qb.head_workspace_bytes(4096, 32000, 4096, nf4=True) >= a + 32000 * 4096 * 2
     assert qb.head_workspace_bytes(4096, 32000, 4096, k=64) > a
     assert qb.head_workspace_bytes(0, 32000, 4096) > 0
+    # whatever piece is asked for, the bytes hold a call: whole tiles of tokens, one at least
+    for M in (1, 100, 256, 257, 900, 5000):
+        sizes = [qb.head_workspace_bytes(M, 1000, 512, piece=p) for p in (1, 100, 255, 256, 300, 512, 1000, 10**6)]
+        assert sizes[0] == sizes[1] == sizes[2] == sizes[3] == sizes[4] and sizes[-1] == qb.head_workspace_bytes(M, 1000, 512)
 
 
 def test_refusals(L):
