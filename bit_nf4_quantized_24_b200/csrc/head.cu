@@ -582,8 +582,9 @@ __global__ void __launch_bounds__(256) k_head_join(const float* __restrict__ spl
 // order), and where each column segment's targets begin.  A slot whose index
 // is outside [0, N) or whose logit is -inf holds nothing: it sorts last.  k is
 // at most 256, so each thread ranks its slot by comparing it with the others.
+constexpr int TARGET_THREADS = 128;
 template <typename T>
-__global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict__ idx, const T* __restrict__ logit,
+__global__ void __launch_bounds__(TARGET_THREADS) k_head_targets(const int64_t* __restrict__ idx, const T* __restrict__ logit,
                                                       int k, int N, float inv_t, int tn, int sw, int nseg,
                                                       int* __restrict__ sidx, float* __restrict__ logq,
                                                       uint16_t* __restrict__ off) {
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
   __shared__ float val[256];
   const int64_t row = blockIdx.x;
   const int s = threadIdx.x;
-  for (int j = s; j < k; j += blockDim.x) {
+  for (int j = s; j < k; j += TARGET_THREADS) {
     const int64_t y = idx[row * k + j];
     const float x = static_cast<float>(logit[row * k + j]);
     const bool kept = y >= 0 && y < N && x != -INFINITY;
@@ -601,13 +602,24 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
     val[j] = x;
   }
   __syncthreads();
+  // maximum and sum over the block, in a fixed order
+  __shared__ float red[2][4];
+  const int lane = s & 31, warp = s >> 5;
   float mx = -INFINITY, sum = 0.0f;
-  for (int j = 0; j < k; ++j)
+  for (int j = s; j < k; j += TARGET_THREADS)
     if (key[j] != kNoTarget) mx = fmaxf(mx, val[j]);
-  for (int j = 0; j < k; ++j)
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (lane == 0) red[0][warp] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  for (int j = s; j < k; j += TARGET_THREADS)
     if (key[j] != kNoTarget) sum += expf((val[j] - mx) * inv_t);
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   const float lsum = logf(sum);
-  for (int j = s; j < k; j += blockDim.x) {
+  for (int j = s; j < k; j += TARGET_THREADS) {
     const int mine = key[j];
     int rank = 0;
     for (int o = 0; o < k; ++o) rank += (key[o] < mine || (key[o] == mine && o < j)) ? 1 : 0;
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(256) k_head_targets(const int64_t* __restrict_
     logq[row * k + rank] = mine == kNoTarget ? -INFINITY : (val[j] - mx) * inv_t - lsum;
   }
   __syncthreads();
-  for (int t = s; t <= nseg; t += blockDim.x) {
+  for (int t = s; t <= nseg; t += TARGET_THREADS) {
     const int64_t bound = min(static_cast<int64_t>(t >> 1) * tn + (t & 1) * sw, static_cast<int64_t>(N));
     int lo = 0, hi = k;  // first slot with sorted >= bound
     while (lo < hi) {
@@ -733,15 +745,19 @@ __device__ __noinline__ void rescale_row(const StatArgs& p, int row, float r, in
   __syncwarp();
 }
 
-// Joins the segments' (reference, sum) pairs of 8 rows per block: first thread
-// (r, j) takes row r and segments j, j + 64, ..., then warp r joins its row's 64
+// Joins the segments' (reference, sum) pairs of SROWS rows per block: first thread
+// (r, j) takes row r and segments j, j + SLANES, ..., then warp r joins its row's
 // values, adds the label's logit or the teacher's terms of the loss, and writes the
 // teacher's columns of e.  The orders are fixed.  The label's logit is one more dot
 // product of X and W with fp32 additions rounded to nearest (12 us for 4096 x 4096,
 // read from HBM): the tensor core's truncating sum alone made the loss of 2047 x
 // 50003 x 2048 1.4e-6 off instead of 4e-7.
-constexpr int SROWS = 8, SLANES = 64;
-__global__ void __launch_bounds__(SROWS * SLANES) k_head_stats(const __grid_constant__ StatArgs p) {
+// 16 rows per block where there are many (4096 tokens: 18 us, with 8 21 us), 4 where
+// a row's chain of segments counts.
+constexpr int STAT_THREADS = 512;
+template <int SROWS>
+__global__ void __launch_bounds__(STAT_THREADS) k_head_stats(const __grid_constant__ StatArgs p) {
+  constexpr int SLANES = STAT_THREADS / SROWS;
   if (p.e) pdl_trigger();  // without a gradient this is the call's last kernel
   pdl_wait();
   __shared__ float2 sh[SROWS][SLANES + 1];
@@ -768,10 +784,13 @@ __global__ void __launch_bounds__(SROWS * SLANES) k_head_stats(const __grid_cons
   const int a = threadIdx.x & 31, b = threadIdx.x >> 5;
   const int row = row0 + b;
   if (b >= SROWS || row >= p.rows) return;
-  const float2 v = sh[b][a], w = sh[b][a + 32];
-  m = fmaxf(v.x, w.x);
+  m = -INFINITY;
+#pragma unroll
+  for (int j = a; j < SLANES; j += 32) m = fmaxf(m, sh[b][j].x);
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  s = v.y * shift2(v.x, m) + w.y * shift2(w.x, m);
+  s = 0.0f;
+#pragma unroll
+  for (int j = a; j < SLANES; j += 32) s += sh[b][j].y * shift2(sh[b][j].x, m);
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   big = own[b] != 0;
   RowStat st{m, 0.0f, big ? m : 0.0f};
@@ -1138,7 +1157,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     p.k = a.k;
     p.ztgt = s.ztgt;
     if (distill) {
-      const dim3 grid(static_cast<unsigned>(rows)), block(std::max(128, (a.k + 31) / 32 * 32));
+      const dim3 grid(static_cast<unsigned>(rows)), block(TARGET_THREADS);
       const int64_t* idx = a.teacher_idx + r0 * a.k;
       const float inv_t = 1.0f / a.temperature;
       if (a.teacher_bf16)
@@ -1177,8 +1196,10 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     t.lde = lde;
     t.tn = seg.tn;
     t.sw = seg.sw;
-    err = launch_ex(k_head_stats, dim3(static_cast<unsigned>((rows + SROWS - 1) / SROWS)), dim3(SROWS * SLANES), 0, st,
-                    true, t);
+    if (rows > 1024)
+      err = launch_ex(k_head_stats<16>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(STAT_THREADS), 0, st, true, t);
+    else
+      err = launch_ex(k_head_stats<4>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(STAT_THREADS), 0, st, true, t);
     if (err != cudaSuccess) return err;
     if (!grad) continue;
     HeadEpi q{};
