@@ -61,9 +61,9 @@ constexpr CUtensorMapSwizzle narrow_swizzle() {
 // RS_WARPS warps each take whole 64-wide k groups.  The warps of a CTA meet
 // in shared memory, the CTAs through distributed shared memory, where CTA 0
 // adds the cluster's partials in a fixed order and writes the outputs.  Each
-// CTA lets the next kernel of the stream launch at once (programmatic
-// dependent launch); that kernel waits for this grid to finish before it
-// reads the outputs.
+// CTA lets the next kernel of the stream launch as soon as the kernel before
+// this one is complete (programmatic dependent launch); that kernel waits for
+// this grid to finish before it reads the outputs.
 constexpr int RS_CTAS = 8, RS_WARPS = 8;
 
 __device__ __forceinline__ uint32_t ldg32(const uint16_t* p) {
@@ -82,8 +82,8 @@ __global__ void __cluster_dims__(RS_CTAS, 1, 1) __launch_bounds__(RS_WARPS * 32)
                  float* __restrict__ out32) {
   __shared__ float wpart[RS_WARPS][16 * 64];
   __shared__ float cpart[16 * 64];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
   const int worker = rank * RS_WARPS + warp;
@@ -161,8 +161,8 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
 __global__ void __launch_bounds__(256) k_dropout_input(const uint16_t* __restrict__ X,
                                                        const uint8_t* __restrict__ mask, float keep, int64_t n8,
                                                        uint16_t* __restrict__ Xd) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= n8) return;
   const uint4 x = __ldg(reinterpret_cast<const uint4*>(X) + i);
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(256) k_dx_add_masked(uint16_t* __restrict__ dX
                                                        const uint16_t* __restrict__ A,
                                                        const uint8_t* __restrict__ mask, float keep, int64_t M,
                                                        int64_t K, int r) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;  // 8-element chunk
   if (i >= M * K / 8) return;
   const int64_t m = (8 * i) / K, k0 = 8 * i - m * K;
@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(256) k_rows_multi(const uint16_t* __restrict__
                                                     const float* __restrict__ scales,
                                                     const int32_t* __restrict__ aidx, uint16_t* __restrict__ Hs) {
   __shared__ float red[8][8];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int m = blockIdx.x, j0 = blockIdx.y * 8;
   const int a = aidx[m];
   const bool ok = a >= 0 && a < na;
@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(32 * (NT + 1)) k_rows(const __grid_constant__ 
   constexpr int RW_ST = S::ST;
   constexpr int CW = S::CW;
   constexpr int RJ = NT * 8;  // j extent of the partial buffer
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t full0 = base + S::OFF_BAR, empty0 = full0 + 8u * RW_ST;
@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(RT_THREADS, 2) k_rows_tc(const __grid_constant
                                                           float sa, uint16_t* __restrict__ out16a, float sb,
                                                           uint16_t* __restrict__ out16b, float* __restrict__ out32,
                                                           int nsplit, int* status) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -746,8 +746,8 @@ __global__ void __launch_bounds__(RT_THREADS, 2) k_cols_tc(const __grid_constant
                                                           const __grid_constant__ CUtensorMap tmG, int M, int C,
                                                           float scale, int transpose, uint16_t* __restrict__ out,
                                                           int nsplit, int* status) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -943,8 +943,8 @@ __global__ void __launch_bounds__(ColsCfg<NT, CB, MASK>::THREADS) k_cols(const _
   // part[j][cl].
   auto pswz = [](int cl) { return (cl << 1) & (RJ - 1); };
   constexpr int MT = S::MT, CWC = S::CWC, ST = S::ST;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t full0 = base + S::OFF_BAR, empty0 = full0 + 8u * ST;

@@ -260,8 +260,14 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
 // are visible; it returns at once when this kernel was launched without the
 // programmatic-serialization attribute.  Every kernel that is launched with the
 // attribute calls pdl_wait (at least in one thread of each CTA) before it
-// reads or overwrites anything an earlier kernel of the layer touches, and
-// before it exits, so that its completion implies that of all earlier kernels.
+// reads or overwrites anything the kernel before it touches, and before it
+// exits, so that its completion implies that of all earlier kernels.
+// k_nf4_gemm, k_gemv and k_gemv_tiles read their activations and write split
+// tiles' partial sums before their pdl_wait.  So each of them is launched behind
+// an adapter kernel (adapter.cu), and every adapter kernel calls pdl_trigger
+// only after its own pdl_wait: when they start, all that precedes that adapter
+// kernel (the previous layer's output among it) is complete, and only what the
+// adapter kernel itself writes has to be waited for.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -217,8 +217,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       // The tail operands come from the previous kernel of the stream, which
       // may still be running (programmatic dependent launch); every other
-      // input of this kernel predates it.  Waited for on every path, so that
-      // this grid completes only after its predecessor.
+      // input of this kernel predates it: that kernel lets this one start only
+      // once all before it is complete (common.cuh).  Waited for on every path,
+      // so that this grid completes only after its predecessor.
       pdl_wait();
       if (ok && has_tail) {  // tail stage: LoRA operands
         const int it = nloc, s = it % STAGES;

@@ -142,9 +142,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int STAGE_BYTES = A_BYTES + NH * B_BYTES;
   constexpr int STAGES = RING_BYTES / STAGE_BYTES;
   static_assert(STAGES <= MAX_STAGES, "barrier block");
-  // The last kernel of a call lets nothing start early: the layer's GEMM, launched
-  // early itself, reads its activations (this call's dX, say) without waiting for
-  // more than the kernel before it has begun.
+  // The last kernel of a call lets nothing start early: whatever follows waits for
+  // its outputs first.
   if (MODE == 0 || g.ntail > 0) pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);

@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ spli
                                                   const uint8_t* __restrict__ codes,
                                                   const uint8_t* __restrict__ absmax_q,
                                                   const float* __restrict__ dq_scale, Nf4Levels lv, int lg, int dq) {
-  pdl_wait();  // no early launch of the next call's kernels: this is the call's last
+  pdl_wait();  // the call's last kernel: it lets nothing start early (see k_head)
   const int c = (blockIdx.x * 128 + threadIdx.x) * 4, row = blockIdx.y;
   if (c >= p.cols) return;
   const int64_t at = static_cast<int64_t>(row) * p.cols + c, piece = static_cast<int64_t>(p.rows) * p.cols;
