@@ -287,16 +287,18 @@ int run_head(HeadArgs& a, const uint16_t* W, const uint8_t* codes, const uint8_t
   const void* words[] = {a.labels, a.teacher_idx};
   for (const void* p : words)
     if (p && !aligned(p, 8)) return QLORA_ERR_SHAPE;
-  const void* floats[] = {dloss, loss, lse, dq_scale, a.teacher_bf16 ? nullptr : a.teacher_logits};
+  const void* floats[] = {dloss, loss, lse, codes ? dq_scale : nullptr, a.teacher_bf16 ? nullptr : a.teacher_logits};
   for (const void* p : floats)
     if (p && !aligned(p, 4)) return QLORA_ERR_SHAPE;
   if (a.teacher_bf16 && !aligned(a.teacher_logits, 2)) return QLORA_ERR_SHAPE;
   a.W = W;
-  a.codes = codes;
-  a.absmax_q = absmax_q;
-  a.dq_scale = dq_scale;
-  a.block = block;
-  a.dq_block = dq_block;
+  if (codes) {  // with a bf16 head nothing below sees the NF4 arguments
+    a.codes = codes;
+    a.absmax_q = absmax_q;
+    a.dq_scale = dq_scale;
+    a.block = block;
+    a.dq_block = dq_block;
+  }
   a.M = M;
   a.N = N;
   a.K = K;
