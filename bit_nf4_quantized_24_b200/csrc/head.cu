@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < SEG; ++j) mx = fmaxf(mx, z[j]);
         // The segment's reference in units of log2 is a whole number, so taking it
-        // off and putting it back are exact.  (A segment whose logits are all -inf
-        // or NaN is summed around 0.)
-        const float ref = mx == -INFINITY ? 0.0f : rintf(mx * p.c);
+        // off and putting it back are exact.  (A segment whose logits are all -inf,
+        // times 1 / T, or NaN has none and is summed around 0.)
+        const float top = rintf(mx * p.c), ref = top == -INFINITY ? 0.0f : top;
         const float back = exp2f(fabsf(ref) <= kHeadFits ? ref : 0.0f);  // e is stored relative to 0, or to ref
         const __nv_bfloat162 back2 = __float2bfloat162_rn(back);
         // The teacher's slots, from the registers: only a warp with a slot in this
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int64_t col = n0 + cwidth; col < p.lde; col += 8)
             *reinterpret_cast<uint4*>(p.e + static_cast<int64_t>(row) * p.lde + col) = make_uint4(0u, 0u, 0u, 0u);
         if (live)
-          p.part[(2 * static_cast<int64_t>(nt) + h) * p.rows + row] = make_float2(mx == -INFINITY ? mx : ref, sum);
+          p.part[(2 * static_cast<int64_t>(nt) + h) * p.rows + row] = make_float2(top, sum);
       } else {
         const float4 f = live && tail < 0 ? p.rscale[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const int label = live && tail < 0 ? __float_as_int(f.w) : -1;
@@ -810,19 +810,21 @@ __global__ void __launch_bounds__(STAT_THREADS) k_head_stats(const __grid_consta
 #pragma unroll 4
         for (int j = a; j < p.K / 8; j += 32) z = dot8(x[j], u[j], z);
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        ny = rintf(z * p.c);
-        zy = fmaf(z, p.c, -ny);
+        const float2 zn = log2_parts(z, p.c);
+        zy = zn.x;
+        ny = zn.y;
       } else {
         const float2 z = p.ztgt[row];
         zy = z.x;
         ny = z.y;
       }
-      // log2 of p / (1 - p): the sums hold the other entries alone
+      // log2 of p / (1 - p): the sums hold the other entries alone.  (A label at -inf
+      // has p = 0 and the loss +inf; if the others are there too, NaN.)
       const float odds = (zy + (ny - m)) - log2f(s);
       total = log1pf(exp2f(-fabsf(odds))) + (odds < 0.0f ? -odds * kLn2 : 0.0f);
       d = expm1f(-total);
       const float top = fmaxf(m, ny);
-      s = s * shift2(m, top) + exp2f(zy + (ny - top));
+      s = s * shift2(m, top) + (ny == -INFINITY ? 0.0f : exp2f(zy + (ny - top)));
       st.m = top;
     }
     st.l2s = log2f(s);

@@ -48,6 +48,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// A logit times c = log2(e) / T as the sum of a whole number, .y, and what is left
+// of it, .x.  A logit of -inf (or one that 1 / T takes there) has .y = -inf and
+// .x = 0, so that differences from .y stay numbers; +inf and NaN give NaN.
+__device__ __forceinline__ float2 log2_parts(float z, float c) {
+  const float n = rintf(z * c);
+  return make_float2(n == -INFINITY ? 0.0f : fmaf(z, c, -n), n);
+}
+
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
           // The warp's four tokens together: each step is a chain of shuffles.
           constexpr int TW = BUF_TOKENS / 4;
           const int j0 = ew * TW, c0 = 4 * lane;
-          float e[TW][4], ref[TW], sum[TW], mx[TW], zy[TW];
+          float e[TW][4], ref[TW], top[TW], sum[TW], mx[TW], zy[TW];
           int label[TW];  // the token's label in this tile (its logit: zy), or -1
 #pragma unroll
           for (int u = 0; u < TW; ++u) {
@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
             for (int u = 0; u < TW; ++u) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], d));
 #pragma unroll
           for (int u = 0; u < TW; ++u) {
-            ref[u] = mx[u] == -INFINITY ? 0.0f : rintf(mx[u] * p.c);  // as in head.cu
+            top[u] = rintf(mx[u] * p.c);  // as in head.cu
+            ref[u] = top[u] == -INFINITY ? 0.0f : top[u];
 #pragma unroll
             for (int q = 0; q < 4; ++q) e[u][q] = exp2_fast(fmaf(e[u][q], p.c, -ref[u]));
             sum[u] = (e[u][0] + e[u][1]) + (e[u][2] + e[u][3]);
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
             const int j = j0 + u, row = m + j;
             if (row >= tokens) break;
             if (lane == 0)
-              p.part[static_cast<int64_t>(nt) * tokens + row] = make_float2(mx[u] == -INFINITY ? mx[u] : ref[u], sum[u]);
+              p.part[static_cast<int64_t>(nt) * tokens + row] = make_float2(top[u], sum[u]);
             if (p.e) {
               uint16_t* er = p.e + static_cast<int64_t>(row) * p.lde + v0;
               const float back = exp2f(fabsf(ref[u]) <= kHeadFits ? ref[u] : 0.0f);
@@ -332,10 +333,7 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
                   *reinterpret_cast<uint2*>(er + (c - v0)) = make_uint2(0u, 0u);
             }
             if (p.labels) {
-              if (label[u] >= 0 && label[u] / 4 == lane) {
-                const float n = rintf(zy[u] * p.c);
-                p.ztgt[row] = make_float2(fmaf(zy[u], p.c, -n), n);
-              }
+              if (label[u] >= 0 && label[u] / 4 == lane) p.ztgt[row] = log2_parts(zy[u], p.c);
             } else {
               const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.tiles + 1) + nt;
               for (int s = o[0] + lane; s < o[1]; s += 32) {

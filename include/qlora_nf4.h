@@ -364,8 +364,13 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  * [M].  dX: device bf16 [M, K], or NULL for the losses alone.  dloss: device
  * fp32 [M], the gradient of the objective with respect to each loss (a mean
  * over c tokens: 1 / c), or NULL for ones; without dX it must be NULL.  Where
- * dloss[m] is 0 the row of dX is 0.  A NaN or an infinity among a token's
- * logits makes that token's lse, loss and dX NaN; other tokens are untouched.
+ * dloss[m] is 0 the row of dX is 0.  A logit z of -inf has the probability 0:
+ * the token's loss is +inf if it is the label's, or a slot's with weight; if all
+ * its logits are -inf, lse is -inf and loss and dX are NaN.  A NaN or +inf among a
+ * token's logits makes its lse, loss and dX NaN.  Other tokens are untouched by
+ * either (an entry of W that is not finite itself makes its column of dX NaN for
+ * every token, as the sums above do).  With dX, N max |W| must stay below 2^63: W
+ * is multiplied by exponentials of up to 2^64 before their sum is taken off.
  * Logits, statistics and sums are fp32; p is rounded to bf16 before the second
  * product (a label's and a token's largest p - q are not) and dX at the end.  Outputs must not overlap inputs.
  *

@@ -4,7 +4,7 @@ import math
 
 import pytest
 import torch
-from test_head import make, teacher
+from test_head import B16, U, distill_targets, make, teacher, xent_targets
 
 from bit_nf4_quantized_24_b200 import binding as qb
 
@@ -48,3 +48,150 @@ def test_scales_beside_a_bf16_head_are_ignored(L):
     f = ctypes.c_void_p(0x10000)
     for absmax, scale in ((None, None), (f, f), (ctypes.c_void_p(0x10001), ctypes.c_void_p(0x10002))):
         assert L.qlora_head_xent(f, None, absmax, scale, 48, 7, 100, 64, f, 4, f, f, f, f, f, f, 1000, None) == -4
+
+
+def with_gone(W, X, gone, T, q, idx, entropy, dloss):
+    """The definition in 64 bits where the logits in `gone` are -inf, with the tolerances of test_head.reference."""
+    W, X, q, entropy, g = W.double(), X.double(), q.double(), entropy.double(), T * dloss.double()
+    N, K = W.shape
+    z = (X @ W.T / T).masked_fill(gone, -math.inf)
+    lse = torch.logsumexp(z, 1)
+    told = q.sum(1) > 0
+    loss = torch.where(q > 0, q * (lse[:, None] - z.gather(1, idx)), 0.0).sum(1) + entropy
+    loss = T * T * torch.where(told, loss, 0.0)
+    D = (K / 16 + 16) * 2 * U * (X.abs() @ W.abs().T).masked_fill(gone, 0.0).amax(1) / T
+    steps = 160 * U * (z.masked_fill(gone, 0.0).abs().amax(1) + lse.abs() + 1)
+    p = (z - lse[:, None]).exp()
+    t = torch.zeros_like(p).scatter_add_(1, idx, q)
+    dt = (p - t).abs() * 1.01 * B16 + (p + t) * (3 * D + 2 * steps + 64 * U)[:, None] + 2.0**-62
+    dp = p * (1.02 * B16 + (3 * D + 2 * steps)[:, None]) + 2.0**-62
+    g = (g * told)[:, None]
+    dx = g * ((p - t) @ W)
+    tol = g.abs() * (torch.where(t > 0, dt, dp) @ W.abs() + (N / 16 + 80) * 2 * U * ((p + t) @ W.abs())) * 1.01
+    return {"loss": loss, "lse": lse, "dx": dx, "tol_lse": D + steps,
+            "tol_loss": T * T * (2 * D + 2 * steps + 64 * U * entropy.abs()),
+            "tol_dx": tol + dx.abs() * 1.01 * B16 + 1e-38}
+
+
+def compare_with_infinities(got, ref, rows, columns=slice(None)):
+    """What is finite in fp32 within its tolerance, the rest the same infinity."""
+    for name, have in zip(("loss", "lse", "dx"), got):
+        want, tol, have = ref[name][rows], ref["tol_" + name][rows], have[rows]
+        if name == "dx":
+            want, tol, have = want[:, columns], tol[:, columns], have[:, columns]
+        far = torch.isinf(want.float())
+        assert torch.equal(have[far].float(), want[far].float()), name
+        assert torch.isfinite(have[~far]).all(), name
+        worst = ((have.double() - want).abs() / tol)[~far].max().item()
+        assert worst <= 1, f"{name}: {worst:.3g} of the tolerance"
+
+
+BIG = 2.0**100  # times -2^40: past fp32's range, from finite values
+
+
+@gpu
+@pytest.mark.parametrize("distill", [False, True])
+@pytest.mark.parametrize("M,N,gone_at", [(20, 700, (300, 301)), (128, 700, (0, 1)), (300, 1400, (1399, 1400)),
+                                         (20, 1400, (256, 700)), (300, 1400, (512, 1100))])
+def test_logits_of_minus_infinity(L, distill, M, N, gone_at):
+    """Every other token has logits of -inf at some entries (one, or whole segments of 128): they are its label, slots
+    of its teacher, or neither."""
+    K, T = 128, 2.0 if distill else 1.0
+    _, values, X, labels, g = make(M + N, M, N, K)
+    at = torch.arange(*gone_at)
+    W = values.float()
+    W[:, 0] = 0
+    W[at.cuda(), 0] = -(2.0**40)
+    X[:, 0] = 0
+    X[::2, 0] = BIG
+    head = W.bfloat16()
+    gone = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    gone[::2, gone_at[0]:gone_at[1]] = True
+    dloss = torch.rand(M, generator=g).cuda() + 0.5
+    if distill:
+        idx, t = teacher(g, M, N, 6, False)
+        idx[4:, 0] = torch.where(torch.arange(4, M) % 4 < 2, at[0], 7 if at[0] > 7 else N - 1).cuda()
+        targets = distill_targets(idx, t, N, T)
+        got = qb.qlora_head_distill(head, X, idx, t, T, dloss=dloss)
+    else:
+        labels[6:12], labels[5], labels[4] = at[-1], -100, -100
+        targets = xent_targets(labels, N)
+        got = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    ref = with_gone(head, X, gone, T, *targets, dloss)
+    assert torch.isinf(ref["loss"]).sum() >= 3
+    compare_with_infinities(got, ref, slice(None))
+    assert qb.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M", [20, 300])
+def test_an_infinite_weight(L, M):
+    """An entry of W at -inf: that logit is -inf for every token whose value there is positive; the other columns of dX
+    are those of a probability of 0."""
+    N, K, j, c = 700, 128, 333, 5
+    _, values, X, labels, g = make(M, M, N, K)
+    labels[3], labels[4] = j, -100
+    X[:, c] = X[:, c].abs() + 0.5
+    dloss = torch.rand(M, generator=g).cuda() + 0.5
+    finite = values.clone()
+    finite[:, c] = 0
+    gone = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    gone[:, j] = True
+    head = finite.clone()
+    head[j, c] = -math.inf
+    got = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    compare_with_infinities(got, with_gone(finite, X, gone, 1.0, *xent_targets(labels, N), dloss), slice(None),
+                            [k for k in range(K) if k != c])
+    assert got[0][3] == math.inf and got[0][4] == 0 and (got[2][4] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("M", [20, 300])
+def test_all_logits_infinite_and_plus_infinity(L, M):
+    N, K = 700, 128
+    _, values, X, labels, g = make(M, M, N, K)
+    W = values.float()
+    W[:, 0] = -(2.0**20)
+    X[:, 0] = 0
+    head = W.bfloat16()
+    labels[6] = -100
+    idx, t = teacher(g, M, N, 6, False, empty=False)
+    idx[6] = -1
+    dloss = torch.rand(M, generator=g).cuda() + 0.5
+    calls = (lambda x: qb.qlora_head_xent(head, x, labels, dloss=dloss),
+             lambda x: qb.qlora_head_distill(head, x, idx, t, 2.0, dloss=dloss))
+    for call in calls:
+        good = call(X)
+        X2 = X.clone()
+        X2[5:7, 0] = 2.0**120   # every logit -inf
+        X2[10:12, 0] = -(2.0**120)  # every logit +inf
+        loss, lse, dx = call(X2)
+        assert (lse[5:7] == -math.inf).all() and torch.isnan(loss[5]) and torch.isnan(dx[5]).all()
+        assert loss[6] == 0 and (dx[6] == 0).all()
+        assert torch.isnan(loss[10:12]).all() and torch.isnan(lse[10:12]).all() and torch.isnan(dx[10:12]).all()
+        rest = [i for i in range(M) if i not in (5, 6, 10, 11)]
+        assert all(torch.equal(a[rest], b[rest]) for a, b in zip(good, (loss, lse, dx)))
+
+
+@gpu
+@pytest.mark.parametrize("M", [20, 300])
+def test_logits_that_the_temperature_makes_infinite(L, M):
+    """Finite logits of -2^120 over T = 1e-4, in whole segments and as slots."""
+    N, K, T = 1400, 128, 1e-4
+    _, values, X, _, g = make(M, M, N, K)
+    W = values.float()
+    W[:, 0] = 0
+    W[512:900, 0] = -(2.0**40)
+    X[:, 0] = 0
+    X[::2, 0] = 2.0**80
+    head = W.bfloat16()
+    gone = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    gone[::2, 512:900] = True
+    idx, t = teacher(g, M, N, 6, False, empty=False)
+    idx[:, 0] = torch.where(torch.arange(M) % 3 == 0, 600, 3).cuda()
+    t[:, 0] = 20.0
+    dloss = torch.rand(M, generator=g).cuda() + 0.5
+    got = qb.qlora_head_distill(head, X, idx, t, T, dloss=dloss)
+    ref = with_gone(head, X, gone, T, *distill_targets(idx, t, N, T), dloss)
+    assert torch.isinf(ref["loss"]).sum() >= 3
+    compare_with_infinities(got, ref, slice(None))
