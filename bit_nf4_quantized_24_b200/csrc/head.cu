@@ -1076,12 +1076,15 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
   return s;
 }
 
-// Tokens per piece when the caller leaves the choice to the library: with a
-// gradient e takes at most 1 GB, without one the tiles' statistics are small
-// and 16384 tokens go at once.  Pieces of a call are alike, in whole tiles.
-int64_t default_piece(int64_t M, int64_t N, bool grad) {
-  const int64_t most =
-      grad ? std::max<int64_t>(TM, (1ll << 30) / (e_pitch(N) * 2) / TM * TM) : int64_t(64) * TM;
+// Tokens per piece when the caller leaves the choice to the library: as many as
+// e (with a gradient) or the segments' statistics and targets (without) hold in
+// 1 GB, one tile at least, and 16384 at most where only statistics are kept.
+// Pieces of a call are alike, in whole tiles.
+int64_t default_piece(int64_t M, int64_t N, int k, bool distill, bool grad) {
+  const int64_t segs = (N + 63) / 64 + 2;  // never more: tiles of 128 entries, two segments each
+  const int64_t token = grad ? e_pitch(N) * 2 : segs * (distill ? 10 : 8) + int64_t(k) * (distill ? 16 : 8);
+  int64_t most = std::max<int64_t>(TM, (1ll << 30) / token / TM * TM);
+  if (!grad) most = std::min<int64_t>(most, 64 * TM);
   const int64_t pieces = std::max<int64_t>(1, (M + most - 1) / most);
   return std::max<int64_t>(1, std::min<int64_t>(M, ((M + pieces - 1) / pieces + TM - 1) / TM * TM));
 }
@@ -1105,13 +1108,13 @@ cudaError_t launch_pairs(const CUtensorMap& a, const CUtensorMap& b, const CUten
 // that is less than one).
 size_t head_workspace_bytes(int64_t piece, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad,
                             bool nf4) {
-  int64_t rows = default_piece(M, N, grad);
+  int64_t rows = default_piece(M, N, k, distill, grad);
   if (piece > 0) rows = std::min(rows, std::max<int64_t>(piece / TM * TM, TM));
   return std::max<size_t>(256, head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes);
 }
 
 int64_t head_piece(size_t bytes, int64_t M, int64_t N, int64_t K, int k, bool distill, bool grad, bool nf4) {
-  int64_t rows = default_piece(M, N, grad);
+  int64_t rows = default_piece(M, N, k, distill, grad);
   while (rows > 0 && head_space(nullptr, rows, M, N, K, k, distill, grad, nf4).bytes > bytes)
     rows = (rows - 1) / TM * TM;
   return rows;

@@ -376,10 +376,11 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  *
  * workspace: qlora_head_workspace bytes, 256-byte aligned.  Tokens are taken
  * in pieces; with a gradient the workspace holds M' x N bf16 values for a piece
- * of M' tokens.  piece = 0 asks for the bytes of the library's own choice (at
- * most 1 GB of such values), another piece for at most that many tokens at
- * a time, in multiples of 256 (256 at least, or M, if fewer); the calls use the
- * largest such pieces that fit the workspace they get, and return
+ * of M' tokens, without one some 8 to 20 bytes per 128 entries and token.  piece = 0
+ * asks for the bytes of the library's own choice (at most 1 GB of either, or
+ * what 256 tokens take, if that is more), another piece for at most that many
+ * tokens at a time, in multiples of 256 (256 at least, or M, if fewer); the calls
+ * use the largest such pieces that fit the workspace they get, and return
  * QLORA_ERR_WORKSPACE if none does.  k = 0 asks for qlora_head_xent, k >= 1 for
  * qlora_head_distill with k slots; want_dx: dX is not NULL; nf4: an NF4 head.
  * Results do not depend on other work of the device, and repeat bit for bit

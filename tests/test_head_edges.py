@@ -4,7 +4,7 @@ import math
 
 import pytest
 import torch
-from test_head import B16, U, distill_targets, make, teacher, xent_targets
+from test_head import B16, U, compare, distill_targets, make, reference, teacher, xent_targets
 
 from bit_nf4_quantized_24_b200 import binding as qb
 
@@ -195,3 +195,42 @@ def test_logits_that_the_temperature_makes_infinite(L, M):
     ref = with_gone(head, X, gone, T, *distill_targets(idx, t, N, T), dloss)
     assert torch.isinf(ref["loss"]).sum() >= 3
     compare_with_infinities(got, ref, slice(None))
+
+
+def test_workspace_of_large_vocabularies(L):
+    """The default's bounds: 1 GB of exponentials with a gradient, of statistics and targets without, or what 256 tokens
+    take.  Beside the exponentials (2 N bytes a token) lie the targets (16 k) and statistics (N / 8 at most): together at
+    most a quarter of them where N >= 2^15 for k = 256."""
+    GB = 1 << 30
+    for lg in range(10, 25):
+        N = 1 << lg
+        for k in (0, 256):
+            for M in (257, 16384, 1 << 20):
+                few = qb.head_workspace_bytes(256, N, 512, k)
+                if k == 0 or lg >= 15:
+                    assert qb.head_workspace_bytes(M, N, 512, k) <= 1.25 * max(GB, few)
+                few = qb.head_workspace_bytes(256, N, 512, k, want_dx=False)
+                assert qb.head_workspace_bytes(M, N, 512, k, want_dx=False) <= 1.25 * max(GB, few)
+    # an ordinary vocabulary still goes 16384 tokens at a time
+    assert qb.head_workspace_bytes(1 << 20, 128000, 512, want_dx=False) == qb.head_workspace_bytes(
+        16384, 128000, 512, want_dx=False) > qb.head_workspace_bytes(8192, 128000, 512, want_dx=False)
+
+
+@gpu
+def test_losses_of_a_large_vocabulary_in_several_pieces(L):
+    """A vocabulary whose statistics bound the piece: 4609 tokens at 2 M entries go 2560 at a time."""
+    M, N, K = 4609, (1 << 21) + 5, 64
+    nbytes = qb.head_workspace_bytes(M, N, K, want_dx=False)
+    assert nbytes == qb.head_workspace_bytes(M, N, K, want_dx=False, piece=2560) < M * (N / 128) * 8
+    g = torch.Generator("cuda").manual_seed(3)
+    W = (torch.randn(N, K, generator=g, device="cuda") * 0.05).bfloat16()
+    X = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    labels = torch.randint(0, N, (M,), generator=g, device="cuda")
+    labels[:3] = torch.tensor([0, N - 1, N])
+    labels[-2:] = torch.tensor([N - 1, -100])
+    loss, lse, _ = qb.qlora_head_xent(W, X, labels)
+    rows = torch.tensor([0, 1, 2, 255, 256, 2559, 2560, 2561, 4607, 4608, M - 2, M - 1], device="cuda")
+    ref = reference(W, X[rows], 1.0, *xent_targets(labels[rows], N), None, piece=4)
+    compare((loss[rows], lse[rows], None), ref)
+    again = qb.qlora_head_xent(W, X, labels)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse) and torch.isfinite(loss).all()
