@@ -234,3 +234,150 @@ def test_losses_of_a_large_vocabulary_in_several_pieces(L):
     compare((loss[rows], lse[rows], None), ref)
     again = qb.qlora_head_xent(W, X, labels)
     assert torch.equal(again[0], loss) and torch.equal(again[1], lse) and torch.isfinite(loss).all()
+
+
+@gpu
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("M,N,K,k,T,bf16", [
+    (1, 300, 256, 1, 1.0, False), (2, 9, 256, 5, 2.0, True), (37, 9001, 512, 33, 1.5, True), (16, 32000, 1024, 64, 2.0, False),
+    (100, 1031, 256, 256, 0.5, False), (128, 2049, 768, 7, 4.0, True), (200, 1031, 512, 12, 1.0, False),
+    (515, 4099, 256, 100, 2.0, True), (384, 600, 256, 3, 1e-3, False),
+])
+@pytest.mark.parametrize("block,dq", [(32, 0), (32, 256), (64, 256), (128, 0), (256, 256)])
+def test_distill_nf4_head(L, block, dq, M, N, K, k, T, bf16, grad):
+    head, values, X, _, g = make(block + dq + M, M, N, K, block, dq)
+    idx, t = teacher(g, M, N, k, bf16)
+    dloss = torch.randn(M, generator=g).cuda() if grad else None
+    ref = reference(values, X, T, *distill_targets(idx, t, N, T), dloss)
+    got = qb.qlora_head_distill(head, X, idx, t, T, dloss=dloss)
+    compare(got, ref)
+    same = qb.qlora_head_distill(values, X, idx, t, T, dloss=dloss)  # the bf16 values as a head
+    compare(same, ref)
+    if M <= 64 or M > 128:
+        assert all(a is b or torch.equal(a, b) for a, b in zip(got, same))
+    nbytes = qb.head_workspace_bytes(M, N, K, k, grad, True, piece=256)  # a last piece of few tokens on the expanded head
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    compare(qb.qlora_head_distill(head, X, idx, t, T, dloss=dloss, workspace=ws), ref)
+    assert qb.device_status() == 0
+
+
+def of_bytes(nbytes, value):
+    """A workspace of `nbytes` bytes of one value, and a guard behind it."""
+    ws = torch.full((nbytes + 4096,), value, dtype=torch.uint8, device="cuda")
+    ws[nbytes:] = 171
+    return ws
+
+
+@gpu
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M", [1, 16, 17, 100, 128, 129, 256, 257, 390, 700])
+def test_nothing_is_read_that_was_not_written(L, M, nf4):
+    """A workspace of NaNs (0xFF in bf16 and fp32, a label or slot of -1) and one of zeros: the same finite results, at
+    vocabularies around the multiples of all that columns come in."""
+    for N in (1, 31, 32, 33, 63, 64, 65, 111, 113, 127, 128, 129, 159, 161, 223, 225, 255, 256, 257, 500, 513, 895, 1025):
+        for K in (64, 192, 576):
+            head, values, X, labels, g = make(M + N + K, M, N, K, 64 if nf4 else 0)
+            labels[M // 2] = -100 if M > 1 else labels[M // 2]
+            idx, t = teacher(g, M, N, 3, False)
+            dloss = torch.rand(M, generator=g).cuda() + 0.1
+            for w in (None, dloss):
+                for piece in (0, 256):
+                    for k in (0, 3):
+                        nbytes = qb.head_workspace_bytes(M, N, K, k, w is not None, nf4, piece)
+                        got = []
+                        for value in (255, 0):
+                            ws = of_bytes(nbytes, value)
+                            if k:
+                                got.append(qb.qlora_head_distill(head, X, idx, t, 2.0, dloss=w, workspace=ws[:nbytes]))
+                            else:
+                                got.append(qb.qlora_head_xent(head, X, labels, dloss=w, workspace=ws[:nbytes]))
+                            assert (ws[nbytes:] == 171).all(), (N, K, k)
+                        for a, b in zip(*got):
+                            assert a is b or (torch.equal(a, b) and torch.isfinite(a).all()), (N, K, k)
+    assert qb.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("M,piece", [(700, 512), (900, 256), (384, 256)])
+def test_pieces_of_a_workspace_of_nans(L, M, piece):
+    """As in test_head.test_pieces_of_tokens, against the definition."""
+    for N, K in ((1000, 192), (3001, 512), (4097, 64)):
+        head, values, X, labels, g = make(M + N, M, N, K)
+        idx, t = teacher(g, M, N, 9, False)
+        dloss = torch.rand(M, generator=g).cuda()
+        nbytes = qb.head_workspace_bytes(M, N, K, 9, piece=piece)
+        ws = of_bytes(nbytes, 255)
+        got = qb.qlora_head_distill(head, X, idx, t, 2.0, dloss=dloss, workspace=ws[:nbytes])
+        compare(got, reference(values, X, 2.0, *distill_targets(idx, t, N, 2.0), dloss))
+        assert (ws[nbytes:] == 171).all()
+        nbytes = qb.head_workspace_bytes(M, N, K, piece=piece)
+        ws = of_bytes(nbytes, 255)
+        got = qb.qlora_head_xent(head, X, labels, dloss=dloss, workspace=ws[:nbytes])
+        compare(got, reference(values, X, 1.0, *xent_targets(labels, N), dloss))
+        assert (ws[nbytes:] == 171).all()
+
+
+@gpu
+@pytest.mark.slow
+@pytest.mark.parametrize("M", [5, 200])
+def test_offsets_into_a_head_past_32_bits(L, M):
+    """More than 2^31 weights in bf16, in NF4, and (200 tokens) in the copy that an NF4 head is expanded to; entries at
+    both ends are labels, slots, and what single tokens put all their probability on."""
+    N, K, k = 135001, 16384, 3
+    assert N * K > 2**31
+    g = torch.Generator("cuda").manual_seed(9)
+    codes = torch.randint(0, 256, (N * K // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    scale = torch.rand(N * K // 64, generator=g, device="cuda") * 0.02 + 0.01
+    head = qb.NF4Weight(codes, torch.empty(0, dtype=torch.uint8, device="cuda"), scale, N, K, 64, 0)
+    values = qb.nf4_dequantize(head)
+    ends = torch.tensor([0, N - 1, N // 2, 131071, 131072, 131073, N - 2, 7], device="cuda")
+    labels, liked = ends[torch.arange(M, device="cuda") % 8], ends[(torch.arange(M, device="cuda") + 1) % 8]
+    X = torch.randn(M, K, generator=g, device="cuda") * 0.05
+    X = (X + values[liked].float() * (30 / values[liked].float().square().sum(1, keepdim=True))).bfloat16()
+    idx = torch.stack((labels, liked, torch.full_like(labels, -1)), 1)
+    t = torch.randn(M, k, generator=g, device="cuda")
+    dloss = torch.ones(M, device="cuda")
+    z = torch.cat([X.double() @ values[i:i + 15000].double().T for i in range(0, N, 15000)], 1)
+    assert (z.argmax(1) == liked).all()
+    D = ((K / 16 + 16) * 2 * U * X.double().abs().sum(1) * values.abs().max().double())[:, None]
+    for T, targets in ((1.0, xent_targets(labels, N)), (2.0, distill_targets(idx, t, N, 2.0))):
+        call = ((lambda h: qb.qlora_head_xent(h, X, labels, dloss=dloss)) if T == 1.0 else
+                (lambda h: qb.qlora_head_distill(h, X, idx, t, 2.0, dloss=dloss)))
+        a, b = call(head), call(values)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        q, at, entropy = (v.double() if v.is_floating_point() else v for v in targets)
+        lse = torch.logsumexp(z / T, 1)
+        loss = T * T * (entropy + (q * (lse[:, None] - z.gather(1, at) / T)).sum(1))
+        d = (z / T - lse[:, None]).exp().scatter_add_(1, at, -q)
+        dx = T * sum(d[:, i:i + 15000] @ values[i:i + 15000].double() for i in range(0, N, 15000))
+        assert ((a[1] - lse).abs() <= 2 * D[:, 0]).all() and ((a[0] - loss).abs() <= 4 * T * T * D[:, 0]).all()
+        # a wrong row of W anywhere would be an error as large as the row's gradient itself
+        assert ((a[2].double() - dx).norm(dim=1) <= 1e-2 * dx.norm(dim=1)).all()
+
+
+@gpu
+@pytest.mark.slow
+def test_offsets_into_the_exponentials_past_32_bits(L):
+    """A piece of 256 tokens times 8.4 M entries: more than 2^31 exponentials.  Each token puts nearly all its probability
+    on an entry of its own, spread from the first to the last, which is not its label."""
+    M, N, K = 256, (1 << 23) + 4099, 64
+    assert M * N > 2**31
+    g = torch.Generator("cuda").manual_seed(10)
+    W = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    liked = (torch.arange(M, device="cuda") * (N - 1)) // (M - 1)
+    labels = (liked + N // 2) % N
+    X = (W[liked].float() * (40 / W[liked].float().square().sum(1, keepdim=True))).bfloat16()
+    dloss = torch.ones(M, device="cuda")
+    loss, lse, dx = qb.qlora_head_xent(W, X, labels, dloss=dloss)
+    W64 = W.double()
+    for a in range(0, M, 16):
+        s = slice(a, a + 16)
+        z = X[s].double() @ W64.T
+        want = torch.logsumexp(z, 1)
+        D = (K / 16 + 16) * 2 * U * (X[s].double().abs() @ W64.abs().T).amax(1) + 160 * U * (z.abs().amax(1) + want.abs() + 1)
+        assert ((lse[s] - want).abs() <= D).all()
+        assert ((loss[s] - (want - z.gather(1, labels[s, None])[:, 0])).abs() <= 2 * D + 2 * U * loss[s]).all()
+        p = (z - want[:, None]).exp()
+        assert (p.gather(1, liked[s, None]) > 0.9).all()
+        grad = p @ W64 - W64[labels[s]]
+        assert ((dx[s].double() - grad).norm(dim=1) <= 1e-2 * grad.norm(dim=1)).all()
