@@ -126,6 +126,24 @@ def _req(t, dtype, name, shape=None):
     return t
 
 
+def _on_stream(call):
+    """What a call allocates (outputs, workspace) belongs to the stream that uses it: with stream= the whole call runs
+    with that stream current, so that memory which the caller's own stream has still to read is not handed to it, nor
+    its workspace back to the caller's stream while its kernels run."""
+    params = call.__code__.co_argcount  # stream is the last of them
+
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        if len(args) == params:
+            *args, stream = args
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+
+    return run
+
+
 def version() -> int:
     return lib().qlora_version()
 
@@ -168,6 +186,7 @@ class NF4Weight:
         return self.codes.numel() + self.absmax_q.numel() + 4 * self.dq_scale.numel()
 
 
+@_on_stream
 def nf4_quantize(W: torch.Tensor, block: int = BLOCK, dq_block: int = DQ_BLOCK, stream=None) -> NF4Weight:
     _req(W, torch.float32, "W")
     N, K = W.shape
@@ -181,6 +200,7 @@ def nf4_quantize(W: torch.Tensor, block: int = BLOCK, dq_block: int = DQ_BLOCK, 
     return NF4Weight(codes, absmax_q, dq_scale, N, K, block, dq_block)
 
 
+@_on_stream
 def nf4_dequantize(w: NF4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     if out is None:
         out = torch.empty(w.N, w.K, dtype=torch.bfloat16, device=w.codes.device)
@@ -190,6 +210,7 @@ def nf4_dequantize(w: NF4Weight, out: torch.Tensor | None = None, stream=None) -
     return out
 
 
+@_on_stream
 def nf4_merge_lora(w: NF4Weight, A: torch.Tensor, B: torch.Tensor, scale: float, block: int | None = None,
                    dq_block: int | None = None, stream=None) -> NF4Weight:
     """A new NF4 weight holding deq(W) + scale * B A, quantized again (in w's
@@ -229,6 +250,7 @@ def _workspace(nbytes, device, ws):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def qlora_linear_fwd(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: float,
                      save_h: bool = True, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                      stream=None):
@@ -257,6 +279,7 @@ def dropout_workspace_bytes(M, N, K, r) -> int:
     return b.value
 
 
+@_on_stream
 def qlora_linear_fwd_dropout(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: float,
                              keep_mask: torch.Tensor, keep_scale: float, save_h: bool = True, out=None,
                              workspace=None, stream=None):
@@ -280,6 +303,7 @@ def qlora_linear_fwd_dropout(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: 
     return out, H
 
 
+@_on_stream
 def qlora_linear_bwd_dropout(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                              scale: float, keep_mask: torch.Tensor, keep_scale: float, H=None, want_dx=True,
                              workspace=None, stream=None):
@@ -301,6 +325,7 @@ def qlora_linear_bwd_dropout(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A:
     return dX, dA, dB
 
 
+@_on_stream
 def qlora_linear_fwd_multi(w: NF4Weight, X: torch.Tensor, A_all: torch.Tensor, B_all: torch.Tensor,
                            scales: torch.Tensor, adapter_idx: torch.Tensor, out: torch.Tensor | None = None,
                            workspace: torch.Tensor | None = None, stream=None):
@@ -330,6 +355,7 @@ def nf4_decode_tiles_bytes(N: int, K: int) -> int:
     return b.value
 
 
+@_on_stream
 def nf4_decode_tiles(w: NF4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The decode-tile copy of w's codes (uint8, nf4_decode_tiles_bytes(N, K)
     bytes) for qlora_linear_fwd_tiles / qlora_linear_fwd_multi_tiles (the
@@ -342,6 +368,7 @@ def nf4_decode_tiles(w: NF4Weight, out: torch.Tensor | None = None, stream=None)
     return out
 
 
+@_on_stream
 def qlora_linear_fwd_tiles(w: NF4Weight, tiles: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                            scale: float, save_h: bool = True, out: torch.Tensor | None = None,
                            workspace: torch.Tensor | None = None, stream=None):
@@ -366,6 +393,7 @@ def qlora_linear_fwd_tiles(w: NF4Weight, tiles: torch.Tensor, X: torch.Tensor, A
     return out, H
 
 
+@_on_stream
 def qlora_linear_fwd_multi_tiles(w: NF4Weight, tiles: torch.Tensor, X: torch.Tensor, A_all: torch.Tensor,
                                  B_all: torch.Tensor, scales: torch.Tensor, adapter_idx: torch.Tensor,
                                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
@@ -390,6 +418,7 @@ def qlora_linear_fwd_multi_tiles(w: NF4Weight, tiles: torch.Tensor, X: torch.Ten
     return out
 
 
+@_on_stream
 def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                      scale: float, H: torch.Tensor | None = None, want_dx: bool = True,
                      outs=None, workspace: torch.Tensor | None = None, stream=None):
@@ -417,6 +446,7 @@ def qlora_linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.T
     return dX, dA, dB
 
 
+@_on_stream
 def qlora_linear_fwd_noalloc(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: float,
                              save_h: bool = True, out: torch.Tensor | None = None, stream=None):
     """qlora_linear_fwd without a workspace: the library's fixed device scratch

@@ -213,3 +213,53 @@ def test_captured_chain(L, M):
             graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def stream_of(t):
+    """The stream that the allocator holds t's memory for."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's")
+
+
+@gpu
+@pytest.mark.parametrize("M", [4, 64])
+def test_what_a_call_allocates_belongs_to_its_stream(L, M):
+    """With stream= outputs and workspace come from that stream's memory, and memory whose last use on the caller's
+    stream is still to run is not written."""
+    D, r = 1024, 16
+    (q, A, B, s), = layers(55, 1, D, r)
+    g = wl.generator(56)
+    X = torch.randn(M, D, generator=g).bfloat16().cuda()
+    W = torch.randn(D, D, generator=g).cuda()
+    mask = torch.ones(M, D, dtype=torch.uint8, device="cuda")
+    tiles = qb.nf4_decode_tiles(q)
+    aidx, scales = torch.zeros(M, dtype=torch.int32, device="cuda"), torch.ones(1, device="cuda")
+    calls = [lambda st: qb.qlora_linear_fwd(q, X, A, B, s, stream=st),
+             lambda st: qb.qlora_linear_fwd(q, X, A, B, s, True, None, None, st),
+             lambda st: qb.qlora_linear_bwd(q, X, X, A, B, s, stream=st),
+             lambda st: qb.qlora_linear_fwd_dropout(q, X, A, B, s, mask, 1.0, stream=st),
+             lambda st: qb.qlora_linear_bwd_dropout(q, X, X, A, B, s, mask, 1.0, stream=st),
+             lambda st: qb.qlora_linear_fwd_noalloc(q, X, A, B, s, stream=st),
+             lambda st: (qb.nf4_dequantize(q, stream=st), qb.nf4_decode_tiles(q, stream=st)),
+             lambda st: [getattr(qb.nf4_quantize(W, stream=st), n) for n in ("codes", "absmax_q", "dq_scale")],
+             lambda st: [getattr(qb.nf4_merge_lora(q, A, B, s, stream=st), n) for n in ("codes", "absmax_q")]]
+    if M <= 16:
+        calls += [lambda st: qb.qlora_linear_fwd_tiles(q, tiles, X, A, B, s, stream=st),
+                  lambda st: (qb.qlora_linear_fwd_multi(q, X, A[None], B[None], scales, aidx, stream=st),
+                              qb.qlora_linear_fwd_multi_tiles(q, tiles, X, A[None], B[None], scales, aidx, stream=st))]
+    for call in calls:
+        side = torch.cuda.Stream()
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        sums, blocks = [], [torch.full_like(t, 3) for t in want for _ in range(2)]
+        torch.cuda._sleep(20_000_000)  # about 10 ms on the caller's stream
+        for b in blocks:
+            sums.append((b == 3).sum() == b.numel())
+        del blocks, b
+        got = call(side)
+        assert all(stream_of(t) == side.cuda_stream for t in got)
+        torch.cuda.synchronize()
+        assert all(sums) and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert qb.device_status() == 0
