@@ -10,8 +10,8 @@
 //
 // The logits never reach memory.  A product kernel (k_head<0>) leaves, for each
 // row and each column segment of its tiles, a reference near the segment's
-// maximum and the sum of exponentials relative to it, and the target logits it
-// meets, all in fp32 straight from the accumulator; k_head_stats joins them into
+// maximum and the sum of exponentials relative to it, and the logits of the
+// teacher's slots it meets, all in fp32 straight from the accumulator; k_head_stats joins them into
 // lse and loss.  For the gradient the same kernel also writes e = exp(z) in bf16
 // for a piece of the tokens, and k_head<1> multiplies e by W once lse is known:
 // p = e exp(-lse) is a factor of the whole row, so it waits for the epilogue,
@@ -691,22 +691,13 @@ __device__ __forceinline__ int write_targets(uint16_t* er, const RowStat& st, in
   return y;
 }
 
-__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    s = fmaf(__uint_as_float(x[j] << 16), __uint_as_float(y[j] << 16), s);
-    s = fmaf(__uint_as_float(x[j] & 0xffff0000u), __uint_as_float(y[j] & 0xffff0000u), s);
-  }
-  return s;
-}
-
 // What k_head_stats reads and writes.
 struct StatArgs {
   const float2* part;  // [nseg][rows]
   int nseg, rows, N, K;
   const int64_t* labels;           // cross entropy, with
-  const uint16_t *X, *W;           //   the label's logit computed here from these, or (null) in ztgt
+  const uint16_t *X, *W;           //   the label's logit computed here from these, or (null)
+  const float* zlabel;             //   taken from here
   const int* sidx;                 // distillation
   const float* logq;
   int k;
@@ -749,8 +740,8 @@ __device__ __noinline__ void rescale_row(const StatArgs& p, int row, float r, in
 // values, adds the label's logit or the teacher's terms of the loss, and writes the
 // teacher's columns of e.  The orders are fixed.  The label's logit is one more dot
 // product of X and W with fp32 additions rounded to nearest (12 us for 4096 x 4096,
-// read from HBM): the tensor core's truncating sum alone made the loss of 2047 x
-// 50003 x 2048 1.4e-6 off instead of 4e-7.
+// read from HBM; few tokens: beside k_few's products): the tensor core's truncating
+// sum alone made the loss of 2047 x 50003 x 2048 1.4e-6 off instead of 4e-7.
 // 16 rows per block where there are many (4096 tokens: 18 us, with 8 21 us), 4 where
 // a row's chain of segments counts.
 constexpr int STAT_THREADS = 512;
@@ -801,23 +792,9 @@ __global__ void __launch_bounds__(STAT_THREADS) k_head_stats(const __grid_consta
     any = y >= 0 && y < p.N;
     if (any) {
       label = static_cast<int>(y);
-      float zy;  // the label's logit times c, relative to ny
-      float ny;
-      if (p.X) {
-        const uint4* x = reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(row) * p.K);
-        const uint4* u = reinterpret_cast<const uint4*>(p.W + y * p.K);
-        float z = 0.0f;
-#pragma unroll 4
-        for (int j = a; j < p.K / 8; j += 32) z = dot8(x[j], u[j], z);
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        const float2 zn = log2_parts(z, p.c);
-        zy = zn.x;
-        ny = zn.y;
-      } else {
-        const float2 z = p.ztgt[row];
-        zy = z.x;
-        ny = z.y;
-      }
+      const float z = p.X ? dot_row(p.X + static_cast<int64_t>(row) * p.K, p.W + y * p.K, p.K, a) : p.zlabel[row];
+      const float2 zn = log2_parts(z, p.c);
+      const float zy = zn.x, ny = zn.y;  // the label's logit times c, relative to ny
       // log2 of p / (1 - p): the sums hold the other entries alone.  (A label at -inf
       // has p = 0 and the loss +inf; if the others are there too, NaN.)
       const float odds = (zy + (ny - m)) - log2f(s);
@@ -1040,7 +1017,7 @@ struct HeadSpace {
   float2* part;
   float2* ztgt;
   float4* rscale;
-  float *logq, *split;
+  float *zlabel, *logq, *split;
   int* sidx;
   uint16_t *off, *e;
   size_t bytes;
@@ -1061,8 +1038,9 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
                last_segs = last ? static_cast<size_t>(last) * segments(last, N, K).count : 0;
   if (nf4 && rows > kHeadFewTokens) s.w16 = static_cast<uint16_t*>(take(static_cast<size_t>(N) * K * 2));
   s.part = static_cast<float2*>(take(std::max(segs, last_segs) * 8));
-  s.ztgt = static_cast<float2*>(take(static_cast<size_t>(rows) * k * 8));
+  if (!distill) s.zlabel = static_cast<float*>(take(kHeadFewTokens * 4));
   if (distill) {
+    s.ztgt = static_cast<float2*>(take(static_cast<size_t>(rows) * k * 8));
     s.sidx = static_cast<int*>(take(static_cast<size_t>(rows) * k * 4));
     s.logq = static_cast<float*>(take(static_cast<size_t>(rows) * k * 4));
     s.off = static_cast<uint16_t*>(take((std::max(segs, last_segs) + rows) * 2));
@@ -1082,7 +1060,7 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
 // Pieces of a call are alike, in whole tiles.
 int64_t default_piece(int64_t M, int64_t N, int k, bool distill, bool grad) {
   const int64_t segs = (N + 63) / 64 + 2;  // never more: tiles of 128 entries, two segments each
-  const int64_t token = grad ? e_pitch(N) * 2 : segs * (distill ? 10 : 8) + int64_t(k) * (distill ? 16 : 8);
+  const int64_t token = grad ? e_pitch(N) * 2 : segs * (distill ? 10 : 8) + (distill ? int64_t(k) * 16 : 0);
   int64_t most = std::max<int64_t>(TM, (1ll << 30) / token / TM * TM);
   if (!grad) most = std::min<int64_t>(most, 64 * TM);
   const int64_t pieces = std::max<int64_t>(1, (M + most - 1) / most);
@@ -1160,6 +1138,9 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     p.off = s.off;
     p.k = a.k;
     p.ztgt = s.ztgt;
+    p.X = X;
+    p.W = W;
+    p.zlabel = s.zlabel;
     if (distill) {
       const dim3 grid(static_cast<unsigned>(rows)), block(TARGET_THREADS);
       const int64_t* idx = a.teacher_idx + r0 * a.k;
@@ -1186,6 +1167,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     t.labels = p.labels;
     t.X = few ? nullptr : X;
     t.W = W;
+    t.zlabel = s.zlabel;
     t.sidx = s.sidx;
     t.logq = s.logq;
     t.k = a.k;

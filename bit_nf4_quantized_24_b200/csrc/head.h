@@ -19,6 +19,9 @@ struct HeadWeight {
   int64_t N, K;
 };
 
+// log2 of a block's weights (32, 64, 128 or 256).
+inline int block_log2(int block) { return block == 32 ? 5 : block == 64 ? 6 : block == 128 ? 7 : 8; }
+
 // What the products' epilogues read and write (MODE 0: logits, MODE 1: gradient).
 struct HeadEpi {
   int rows;         // token rows of the piece
@@ -32,10 +35,12 @@ struct HeadEpi {
   const int* sidx;           // [rows][k] targets in ascending order, and
   const uint16_t* off;       // [rows][segments + 1] first target of each column segment
   int k;
-  float2* ztgt;              // [rows][k] target logits: (z c - n, n)
+  const uint16_t* X;         // few tokens: the labels' logits are computed beside the products
+  float* zlabel;             // [rows]
+  float2* ztgt;              // [rows][k] the teacher's slots' logits: (z c - n, n)
   // MODE 1: dX = sums x y + z W[w]; y = 0: the row is written as zeros; w < 0: no such term
   const float4* rscale;      // [rows] (x, y, z, w as int)
-  const uint16_t* W;         // bf16 head (few tokens on an NF4 head: null)
+  const uint16_t* W;         // both modes: bf16 head (few tokens on an NF4 head: null)
   uint16_t* out;             // [rows][cols]
   float* split;              // fp32 sums of the split tiles' pieces
 };
@@ -54,6 +59,30 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ float2 log2_parts(float z, float c) {
   const float n = rintf(z * c);
   return make_float2(n == -INFINITY ? 0.0f : fmaf(z, c, -n), n);
+}
+
+// s + the products of eight bf16, with additions rounded to nearest.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    s = fmaf(__uint_as_float(x[j] << 16), __uint_as_float(y[j] << 16), s);
+    s = fmaf(__uint_as_float(x[j] & 0xffff0000u), __uint_as_float(y[j] & 0xffff0000u), s);
+  }
+  return s;
+}
+__device__ __forceinline__ float warp_sum(float z) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  return z;
+}
+// x . w over K bf16 by a warp.
+__device__ __forceinline__ float dot_row(const uint16_t* x, const uint16_t* w, int K, int lane) {
+  float z = 0.0f;
+#pragma unroll 4
+  for (int j = lane; j < K / 8; j += 32)
+    z = dot8(reinterpret_cast<const uint4*>(x)[j], reinterpret_cast<const uint4*>(w)[j], z);
+  return warp_sum(z);
 }
 
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {

@@ -233,6 +233,38 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
     // ------------------------------------------------------------- epilogue
     const int quad = warp & 3, ew = (warp - 2) & 3, set = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    // The labels' logits, a token per warp: fp32 dot products with additions rounded
+    // to nearest, while the first tile's products run.  (Taken from the accumulators,
+    // which truncate, they made the loss of a single confident token up to 9e-6 off,
+    // of 128 tokens and K = 8192 2e-6; in the statistics kernel they took 1 to 8 us.)
+    if (MODE == 0 && p.labels) {
+      for (int row = blockIdx.x + gridDim.x * (warp - 2); row < tokens; row += gridDim.x * 4 * SETS) {
+        const int64_t y = p.labels[row];
+        if (y < 0 || y >= p.cols) continue;
+        const uint4* x = reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(row) * K);
+        float z = 0.0f;
+        for (int j = lane; j < K / 32; j += 32) {  // 32 weights, of one block
+          const int64_t at = y * K + 32 * j, blk = at >> lg;
+          uint4 w[4];
+          if (!NF4) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = ldg_nc_v4(p.W + at + 8 * q);
+          } else {
+            const uint4 c = ldg_nc_v4(codes + at / 2);
+            const float scale = dq ? __fmul_rn(static_cast<float>(absmax_q[blk]), dq_scale[blk >> 8]) : dq_scale[blk];
+            const Nf4Lut lut = make_lut(lv, scale);
+            deq8(c.x, lut, w[0].x, w[0].y, w[0].z, w[0].w);
+            deq8(c.y, lut, w[1].x, w[1].y, w[1].z, w[1].w);
+            deq8(c.z, lut, w[2].x, w[2].y, w[2].z, w[2].w);
+            deq8(c.w, lut, w[3].x, w[3].y, w[3].z, w[3].w);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) z = dot8(x[4 * j + q], w[q], z);
+        }
+        z = warp_sum(z);
+        if (lane == 0) p.zlabel[row] = z;
+      }
+    }
     int t = 0, filled = 0;
     for (int i = blockIdx.x; i < nitems; i += gridDim.x, ++t) {
       int nt, z, kbeg, kend;
@@ -278,8 +310,8 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
           // The warp's four tokens together: each step is a chain of shuffles.
           constexpr int TW = BUF_TOKENS / 4;
           const int j0 = ew * TW, c0 = 4 * lane;
-          float e[TW][4], ref[TW], top[TW], sum[TW], mx[TW], zy[TW];
-          int label[TW];  // the token's label in this tile (its logit: zy), or -1
+          float e[TW][4], ref[TW], top[TW], sum[TW], mx[TW];
+          int label[TW];  // the token's label in this tile, or -1
 #pragma unroll
           for (int u = 0; u < TW; ++u) {
             label[u] = -1;
@@ -295,7 +327,6 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
             mx[u] = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              if (c0 + q == label[u]) zy[u] = e[u][q];
               if (c0 + q >= ncols || c0 + q == label[u]) e[u][q] = -INFINITY;  // a label stays out of the sums
               mx[u] = fmaxf(mx[u], e[u][q]);
             }
@@ -332,9 +363,7 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
                 for (int64_t c = v0 + g.br + c0; c < p.lde; c += 128)
                   *reinterpret_cast<uint2*>(er + (c - v0)) = make_uint2(0u, 0u);
             }
-            if (p.labels) {
-              if (label[u] >= 0 && label[u] / 4 == lane) p.ztgt[row] = log2_parts(zy[u], p.c);
-            } else {
+            if (!p.labels) {
               const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.tiles + 1) + nt;
               for (int s = o[0] + lane; s < o[1]; s += 32) {
                 const int64_t at = static_cast<int64_t>(row) * p.k + s;
@@ -553,8 +582,7 @@ cudaError_t launch_kind(const CUtensorMap& w, const CUtensorMap& x, const FewGri
                         const HeadWeight& h, cudaStream_t st) {
   cudaError_t e = smem_limit_once<k_few<MODE, KIND>>(SMEM_MAX);
   if (e != cudaSuccess) return e;
-  int lg = 0;
-  while ((1 << lg) < h.block) ++lg;
+  const int lg = block_log2(h.block);
   const int grid = std::min(g.tiles * g.nsplit, device_sm_count());
   return launch_ex(k_few<MODE, KIND>, dim3(grid), dim3(threads_of(KIND > 0)), few_smem(g, KIND > 0), st,
                    true, w, x, g, p, h.codes, h.absmax_q, h.dq_scale, host_codebook().levels, static_cast<int>(h.N),
@@ -630,8 +658,7 @@ cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp,
   CUtensorMap w{}, x;
   if ((h.W && !make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, 64, BK, SW128)) ||
       !make_map(&x, BF16, P, ldp, p.rows, ldp * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
-  int lg = 0;
-  while ((1 << lg) < h.block) ++lg;
+  const int lg = block_log2(h.block);
   cudaError_t e = launch_few<1>(w, x, g, p, h, st);
   if (e != cudaSuccess) return e;
   return launch_ex(k_few_join, dim3(static_cast<unsigned>((p.cols + 511) / 512), static_cast<unsigned>(p.rows)),

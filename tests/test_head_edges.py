@@ -7,6 +7,7 @@ import torch
 from test_head import B16, U, compare, distill_targets, make, reference, teacher, xent_targets
 
 from bit_nf4_quantized_24_b200 import binding as qb
+from bit_nf4_quantized_24_b200 import workloads as wl
 
 gpu = pytest.mark.gpu
 
@@ -381,3 +382,30 @@ def test_offsets_into_the_exponentials_past_32_bits(L):
         assert (p.gather(1, liked[s, None]) > 0.9).all()
         grad = p @ W64 - W64[labels[s]]
         assert ((dx[s].double() - grad).norm(dim=1) <= 1e-2 * grad.norm(dim=1)).all()
+
+
+@gpu
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M", [1, 100, 128, 200, 2000])
+def test_logit_of_the_label_is_summed_to_nearest(L, M, nf4):
+    """A label's logit of about -20 out of 16384 products of one sign beside logits of 0, so that the loss is the logit
+    and log(N - 128) alone.  Sums to nearest: a lane adds at most K / 32 products (every fp32 step is off by at most
+    U of a partial sum, which grows evenly: K / 64 U of the whole), then 5 steps join the lanes, and 12 roundings of
+    |loss| follow.  A sum that truncates, K / 16 steps in one to four parts, is off by more in the long run."""
+    N, K = 400, 16384
+    g = wl.generator(M)
+    X = (torch.rand(M, K, generator=g) + 0.25).bfloat16().cuda()
+    W = torch.zeros(N, K)
+    W[:128] = -(torch.rand(128, K, generator=g) + 0.5) * (20 / (0.75 * K))
+    labels = (torch.arange(M) % 128).cuda()
+    head = qb.nf4_quantize(W.cuda()) if nf4 else W.bfloat16().cuda()
+    values = (qb.nf4_dequantize(head) if nf4 else head).double()
+    assert (values[128:] == 0).all()
+    dloss = torch.ones(M, device="cuda")
+    loss, lse, dx = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    z = X.double() @ values.T
+    want = torch.logsumexp(z, 1) - z.gather(1, labels[:, None])[:, 0]
+    assert (z.gather(1, labels[:, None]) < -15).all()
+    tol = (K / 64 + 5) * U * z.gather(1, labels[:, None])[:, 0].abs() + 12 * U * want
+    assert ((loss - want).abs() <= tol).all(), ((loss - want).abs() / tol).max()
+    assert ((lse - torch.logsumexp(z, 1)).abs() <= 12 * U * 6).all()
