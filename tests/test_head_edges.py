@@ -409,3 +409,40 @@ def test_logit_of_the_label_is_summed_to_nearest(L, M, nf4):
     tol = (K / 64 + 5) * U * z.gather(1, labels[:, None])[:, 0].abs() + 12 * U * want
     assert ((loss - want).abs() <= tol).all(), ((loss - want).abs() / tol).max()
     assert ((lse - torch.logsumexp(z, 1)).abs() <= 12 * U * 6).all()
+
+
+def draw_lean(seed, M, N, K, lean):
+    """Hidden states that lean towards their labels and an NF4 head of spread 0.03, as a trained one has."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    codes = torch.randint(0, 256, (N * K // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    scale = 0.052 * (0.7 + 0.6 * torch.rand(N * K // 64, generator=g, device="cuda"))
+    head = qb.NF4Weight(codes, torch.empty(0, dtype=torch.uint8, device="cuda"), scale, N, K, 64, 0)
+    values = qb.nf4_dequantize(head)
+    labels = torch.randint(0, N, (M,), generator=g, device="cuda")
+    rows = values[labels].float()
+    X = torch.randn(M, K, generator=g, device="cuda")
+    X += rows * (lean * torch.rand(M, 1, generator=g, device="cuda") / rows.square().sum(1, keepdim=True))
+    return head, values, X.bfloat16(), labels, g
+
+
+def six_digits(head, values, X, labels, idx, t, T):
+    """Loss and lse of both operators hold six digits over the call: a relative 2-norm error of at most 1e-6."""
+    for got, targets, temp in ((qb.qlora_head_xent(head, X, labels), xent_targets(labels, head.N), 1.0),
+                               (qb.qlora_head_distill(head, X, idx, t, T), distill_targets(idx, t, head.N, T), T)):
+        ref = reference(values, X, temp, *targets, None)
+        for name, g in zip(("loss", "lse"), got):
+            err = ((g.double() - ref[name]).norm() / ref[name].norm()).item()
+            assert err <= 1e-6, f"{name}: {err:.2g}"
+
+
+@gpu
+@pytest.mark.parametrize("K", [2048, 4096, 8192])
+@pytest.mark.parametrize("M,N", [(200, 3000), (900, 1000), (300, 20001)])
+def test_losses_hold_six_digits(L, M, N, K):
+    """The promise of the documents, at the widths where the tensor core's truncating additions would break it: logits
+    have a spread of 0.03 sqrt(K) and sums of K / 16 steps."""
+    head, values, X, labels, g = draw_lean(M + K, M, N, K, 10.0)
+    idx = torch.randint(0, N, (M, 20), generator=g, device="cuda")
+    idx[:, 0] = labels
+    t = 10.0 - 2.0 * torch.arange(1.0, 21.0, device="cuda").log().expand(M, 20).contiguous()
+    six_digits(head, values, X, labels, idx, t, 1.0)
