@@ -58,18 +58,6 @@ constexpr int SMEM_ALLOC = OFF_BAR + 256 + 1024;  // slack for 1024-byte alignme
 constexpr int NUM_THREADS = 64 + EPI_WARPS * 32;
 constexpr int TMEM_COLS = 512;  // two accumulators of 256 columns
 constexpr int kNoTarget = 0x7fffffff;
-// Parts of a logit's contraction of n stages, each of at most 64/3 (1365 of the
-// contraction, 86 of the tensor core's steps): a part fills an accumulator, which
-// the epilogue then adds up in fp32 registers.  The tensor core truncates every
-// addition to an accumulator, always towards 0, so a long sum drifts with its
-// length: products of one sign, in units of 2^-24 of the logit, by 5 after 32
-// steps, 17 after 64, 24 after 85, 54 after 128 and 176 after 256.  The registers'
-// additions round to nearest.  Largest error of the losses over drawn calls of up
-// to 8192 x 131072 x 8192 (2-norm, relative): parts of 85 steps 1.0e-6, of 128
-// 1.5e-6; time of the losses / the step of 4096 x 32000 x 4096 with 64, 85 and 128
-// steps: 760 / 1691, 758 / 1688, 748 / 1687 us under the power cap, and of its
-// distillation step (64 slots) 1742, 1706, 1706 us.
-__host__ __device__ constexpr int parts_of(int n) { return (3 * n + 63) / 64; }
 
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 
@@ -261,7 +249,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int i = first; i < nitems && ok; i += step) {
         int mt, nt, kbeg, kend, tail, z;
         item(i, mt, nt, kbeg, kend, tail, z);
-        const int parts = MODE == 0 ? parts_of(kend - kbeg) : 1;
+        const int parts = MODE == 0 ? parts_of((kend - kbeg) * BK) : 1;
         for (int q = 0, k = kbeg; q < parts && ok; ++q, ++t) {
           const int stop = kbeg + (q + 1) * (kend - kbeg) / parts, start = k;
           if (NH == 1) {
@@ -361,7 +349,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           end_t = o[1];
         }
         float z[SEG];
-        const int parts = parts_of(kend - kbeg);
+        const int parts = parts_of((kend - kbeg) * BK);
         for (int q = 0; q < parts; ++q) {
           if (!(ok = take(a))) break;
           const uint32_t acc = tmem + lane_base + 256u * a + cseg;

@@ -53,7 +53,8 @@ struct FewGrid {
   int numK;    // stages of the contraction (SUB x 64 each)
   int tp;      // tokens, rounded up to 16
   int stages;
-  int parts;   // accumulators that a contraction fills in turn
+  int parts;   // accumulators that a round of the contraction fills in turn
+  int rounds;  // rounds (MODE 0), joined in tp more columns of TMEM if there are several
   int cols;    // TMEM columns
 };
 
@@ -191,9 +192,15 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
     bool ok = true, committed = false;
     RingPos r;
     int t = 0;
-    for (int i = blockIdx.x; i < nitems && ok; i += gridDim.x, ++t) {
-      int nt, z, kbeg, kend;
-      item(i, nt, z, kbeg, kend);
+    for (int i = blockIdx.x, rd = 0; i < nitems && ok; ++t) {
+      int nt, z, ibeg, iend;
+      item(i, nt, z, ibeg, iend);
+      const int kbeg = MODE == 0 ? ibeg + rd * (iend - ibeg) / g.rounds : ibeg;
+      const int kend = MODE == 0 ? ibeg + (rd + 1) * (iend - ibeg) / g.rounds : iend;
+      if (MODE == 1 || ++rd == g.rounds) {
+        rd = 0;
+        i += gridDim.x;
+      }
       if (!(ok = wait_warp(acc_empty(t & 1), ((t >> 1) & 1) ^ 1, abort, status))) break;
       tc_fence_after();
       const uint32_t d0 = tmem + (t & 1) * g.parts * g.tp;
@@ -266,13 +273,42 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
       }
     }
     int t = 0, filled = 0;
-    for (int i = blockIdx.x; i < nitems; i += gridDim.x, ++t) {
+    // A round that is not the contraction's last leaves its sums, with those of the
+    // rounds before, in TMEM, where the same threads find them again.
+    const uint32_t total = tmem + lane_base + 2 * g.parts * g.tp;
+    for (int i = blockIdx.x, rd = 0; i < nitems; ++t) {
       int nt, z, kbeg, kend;
       item(i, nt, z, kbeg, kend);
       // a set's four warps leave together: they meet at barriers
       if (!epilogue_all(set, wait_bounded(acc_full(t & 1), (t >> 1) & 1, abort, status))) break;
       tc_fence_after();
       const uint32_t acc = tmem + lane_base + (t & 1) * g.parts * g.tp;
+      auto sums = [&](int m, uint32_t (&x)[16]) {  // of 16 tokens, as the bits of floats
+        tmem_ld_x16((rd > 0 ? total : acc) + m, x);
+        tmem_ld_wait();
+#pragma unroll 1
+        for (int q = rd > 0 ? 0 : 1; q < g.parts; ++q) {
+          uint32_t v[16];
+          tmem_ld_x16(acc + q * g.tp + m, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) + __uint_as_float(v[j]));
+        }
+      };
+      if (MODE == 0 && rd + 1 < g.rounds) {
+#pragma unroll 1
+        for (int m = 16 * set; m < tokens; m += 16 * SETS) {
+          uint32_t x[16];
+          sums(m, x);
+          tmem_st_x16(total + m, x);
+        }
+        tmem_st_wait();
+        ++rd;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(t & 1));
+        continue;
+      }
       if (MODE == 1) {
         const int k = nt * UM + quad * 32 + lane;
         float* dst = p.split + static_cast<int64_t>(z) * tokens * p.cols + k;
@@ -297,14 +333,11 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
           // has a token's entries side by side
           const uint32_t b = buf + set * BUF_BYTES + (filled & 1) * (BUF_BYTES / 2);
           float* bp = reinterpret_cast<float*>(smem_raw + (b - raw));
-          for (int q = 0; q < g.parts; ++q) {
-            uint32_t v[16];
-            tmem_ld_x16(acc + q * g.tp + m, v);
-            tmem_ld_wait();
-            float* x = bp + quad * 32 + lane;
+          {
+            uint32_t x[BUF_TOKENS];
+            sums(m, x);
 #pragma unroll
-            for (int j = 0; j < BUF_TOKENS; ++j)
-              x[j * BUF_PITCH] = q == 0 ? __uint_as_float(v[j]) : x[j * BUF_PITCH] + __uint_as_float(v[j]);
+            for (int j = 0; j < BUF_TOKENS; ++j) bp[j * BUF_PITCH + quad * 32 + lane] = __uint_as_float(x[j]);
           }
           epilogue_barrier(set);
           // The warp's four tokens together: each step is a chain of shuffles.
@@ -376,6 +409,8 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty(t & 1));
+      rd = 0;
+      i += gridDim.x;
     }
   } else if (NF4) {
     // ----------------------------------------------- expansion of the codes
@@ -564,16 +599,34 @@ int few_smem(const FewGrid& g, bool nf4) {
   return 1024 + g.stages * SUB * (W_BYTES + g.tp * BK * 2) + epi_sets(nf4) * BUF_BYTES + BAR_BYTES;
 }
 
-FewGrid few_grid(int64_t tokens, int parts, bool nf4) {
+// contraction: that of a logit, K (0: the gradient's, which is not divided: its
+// terms have both signs and its result is rounded to bf16).
+FewGrid few_grid(int64_t tokens, int64_t contraction, bool nf4) {
   FewGrid g{};
   g.tp = static_cast<int>((tokens + 15) / 16 * 16);
   g.stages = few_stages(g.tp, nf4);
-  // A logit's contraction fills several accumulators in turn, which the epilogue
-  // adds up: up to 8, while two sets fit TMEM, each for at least 256 of it (the
-  // tensor core's additions truncate, see CHUNK in head.cu).
-  g.parts = std::max(1, std::min(parts, 256 / g.tp));
+  g.parts = g.rounds = 1;
+  if (contraction > 0) {
+    // A logit's contraction fills several accumulators in turn, which the epilogue
+    // adds up (the tensor core's additions truncate, see parts_of): as many as two
+    // sets of them leave room for in TMEM, up to 8 of at least 256 of the
+    // contraction, or 16 of 512.  Where these are too few for parts_of, it goes in
+    // rounds, with room for one set's total.  (One round left errors of 2.5e-6 in the
+    // losses of 128 tokens at K = 8192.  On 32000 entries, one round / three: 128
+    // tokens, NF4 head, K = 4096 59.1 / 62.8 us; one / six: 128 tokens, bf16 head, K =
+    // 8192 102 / 105 us, with the gradient 232 / 235 us.)
+    const int64_t want = std::max(std::min<int64_t>((contraction + 255) / 256, 8),
+                                  std::min<int64_t>((contraction + 511) / 512, 16));
+    const int64_t need = parts_of(static_cast<int>(contraction));
+    g.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, 256 / g.tp)));
+    if (g.parts < need) {
+      g.parts = (512 / g.tp - 1) / 2;
+      g.rounds = static_cast<int>((need + g.parts - 1) / g.parts);
+    }
+  }
+  const int used = (2 * g.parts + (g.rounds > 1 ? 1 : 0)) * g.tp;
   g.cols = 32;
-  while (g.cols < 2 * g.parts * g.tp) g.cols *= 2;
+  while (g.cols < used) g.cols *= 2;
   return g;
 }
 
@@ -637,7 +690,7 @@ int few_splits(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, const HeadEpi& p, cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, static_cast<int>(std::min<int64_t>((h.K + 255) / 256, 8)), !h.W);
+  FewGrid g = few_grid(p.rows, h.K, !h.W);
   g.br = br;
   g.tiles = static_cast<int>((h.N + br - 1) / br);
   g.nsplit = 1;
@@ -650,7 +703,7 @@ cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, co
 
 cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp, int nsplit, const HeadEpi& p,
                             cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, 1, !h.W);
+  FewGrid g = few_grid(p.rows, 0, !h.W);
   g.br = UM;
   g.tiles = static_cast<int>((h.K + UM - 1) / UM);
   g.nsplit = nsplit;

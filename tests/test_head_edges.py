@@ -427,8 +427,9 @@ def draw_lean(seed, M, N, K, lean):
 
 def six_digits(head, values, X, labels, idx, t, T):
     """Loss and lse of both operators hold six digits over the call: a relative 2-norm error of at most 1e-6."""
-    for got, targets, temp in ((qb.qlora_head_xent(head, X, labels), xent_targets(labels, head.N), 1.0),
-                               (qb.qlora_head_distill(head, X, idx, t, T), distill_targets(idx, t, head.N, T), T)):
+    N = values.shape[0]
+    for got, targets, temp in ((qb.qlora_head_xent(head, X, labels), xent_targets(labels, N), 1.0),
+                               (qb.qlora_head_distill(head, X, idx, t, T), distill_targets(idx, t, N, T), T)):
         ref = reference(values, X, temp, *targets, None)
         for name, g in zip(("loss", "lse"), got):
             err = ((g.double() - ref[name]).norm() / ref[name].norm()).item()
@@ -446,3 +447,36 @@ def test_losses_hold_six_digits(L, M, N, K):
     idx[:, 0] = labels
     t = 10.0 - 2.0 * torch.arange(1.0, 21.0, device="cuda").log().expand(M, 20).contiguous()
     six_digits(head, values, X, labels, idx, t, 1.0)
+
+
+@gpu
+@pytest.mark.parametrize("M,K", [(16, 8192), (33, 8192), (64, 4096), (64, 8192), (66, 4096), (96, 6080), (100, 8192),
+                                 (113, 4096), (128, 2048), (128, 4096), (128, 8192), (128, 16384)])
+@pytest.mark.parametrize("N", [1000, 20001])
+def test_losses_of_few_tokens_hold_six_digits(L, N, M, K):
+    head, values, X, labels, g = draw_lean(M + K, M, N, K, 10.0)
+    idx = torch.randint(0, N, (M, 20), generator=g, device="cuda")
+    idx[:, 0] = labels
+    t = 10.0 - 2.0 * torch.arange(1.0, 21.0, device="cuda").log().expand(M, 20).contiguous()
+    for h in (head, values):  # NF4 and bf16
+        six_digits(h, values, X, labels, idx, t, 1.0)
+
+
+@gpu
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M,N,K", [(17, 300, 8256), (48, 5000, 4160), (48, 5000, 8192), (64, 300, 4160), (64, 40, 12352),
+                                   (80, 700, 2112), (80, 19000, 4096), (97, 33333, 4160), (112, 1000, 8192), (113, 500, 2112),
+                                   (128, 2000, 3136), (128, 20001, 4096), (128, 130, 16448)])
+def test_contraction_in_rounds(L, M, N, K, nf4):
+    """Few tokens whose contraction goes in rounds, several tiles per block among them, with the gradient."""
+    head, values, X, labels, g = make(M + N + K, M, N, K, 64 if nf4 else 0, w_std=0.02)
+    labels[1], labels[2] = -100, N
+    idx, t = teacher(g, M, N, 7, False)
+    dloss = torch.randn(M, generator=g).cuda()
+    got = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    compare(got, reference(values, X, 1.0, *xent_targets(labels, N), dloss))
+    again = qb.qlora_head_xent(head, X, labels, dloss=dloss)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    compare(qb.qlora_head_distill(head, X, idx, t, 2.0, dloss=dloss),
+            reference(values, X, 2.0, *distill_targets(idx, t, N, 2.0), dloss))
+    assert qb.device_status() == 0
