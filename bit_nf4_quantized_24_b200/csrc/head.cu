@@ -641,11 +641,11 @@ struct RowStat {
 };
 
 // Writes p - q, relative to reference r, into the columns of the row's teacher
-// slots (one warp per row), all but the largest one: that one stays in fp32 (*d, and
+// slots (one warp per row; what the rounding leaves into el, if given), all but the largest one: that one stays in fp32 (*d, and
 // its entry as the result) and is added in the gradient's epilogue as a label's is.
 // (The slots' rounding to bf16 alone makes the error of dX 1.4 times that of a bf16
 // result, and the largest slot has most of it.)
-__device__ __forceinline__ int write_targets(uint16_t* er, const RowStat& st, int lane, int row, const int* sidx,
+__device__ __forceinline__ int write_targets(uint16_t* er, uint16_t* el, const RowStat& st, int lane, int row, const int* sidx,
                                              const float* logq, int k, const float2* ztgt, float* d_out) {
   const float up = exp2f((st.m - st.r) + st.l2s);
   const int64_t at = static_cast<int64_t>(row) * k;
@@ -658,7 +658,9 @@ __device__ __forceinline__ int write_targets(uint16_t* er, const RowStat& st, in
     const float2 z = ztgt[at + j];
     float d = exp2f((z.x + (z.y - st.m)) - st.l2s);
     for (int o = j; o < k && sidx[at + o] == y; ++o) d -= expf(logq[at + o]);
-    er[y] = static_cast<uint16_t>(bf16x2_bits(d * up, 0.0f));
+    const uint32_t hi = bf16x2_bits(d * up, 0.0f);
+    er[y] = static_cast<uint16_t>(hi);
+    if (el) el[y] = static_cast<uint16_t>(bf16x2_bits(d * up - __uint_as_float(hi << 16), 0.0f));
     if (fabsf(d) > fabsf(best)) {
       best = d;
       entry = y;
@@ -675,7 +677,10 @@ __device__ __forceinline__ int write_targets(uint16_t* er, const RowStat& st, in
       y = y2;
     }
   }
-  if (y >= 0 && entry == y) er[y] = 0;
+  if (y >= 0 && entry == y) {
+    er[y] = 0;
+    if (el) el[y] = 0;
+  }
   *d_out = d;
   return y;
 }
@@ -696,6 +701,7 @@ struct StatArgs {
   float *loss, *lse;
   float4* rscale;
   uint16_t* e;  // null: no gradient
+  uint16_t* e_low;  // the second part of a teacher's p - q (nullable)
   int64_t lde;
   int tn, sw;   // column segments of e (see Segments)
 };
@@ -811,7 +817,7 @@ __global__ void __launch_bounds__(STAT_THREADS) k_head_stats(const __grid_consta
   const float g = any ? (p.dloss ? p.dloss[row] : 1.0f) * p.temp : 0.0f;
   if (p.e && g != 0.0f) {  // otherwise the row's gradient is written as zeros
     if (big) rescale_row(p, row, st.r, a);
-    if (!p.labels) label = write_targets(p.e + row * p.lde, st, a, row, p.sidx, p.logq, p.k, p.ztgt, &d);
+    if (!p.labels) label = write_targets(p.e + row * p.lde, p.e_low ? p.e_low + row * p.lde : nullptr, st, a, row, p.sidx, p.logq, p.k, p.ztgt, &d);
   }
   if (a == 0) {
     p.loss[row] = any ? total * (p.temp * p.temp) : 0.0f;
@@ -990,10 +996,13 @@ Segments segments(int64_t rows, int64_t N, int64_t K) {
   return {g.tn, g.sw, 2 * g.ntiles};
 }
 
+bool two_parts(int64_t rows, bool distill) { return distill && rows <= kHeadTwoParts; }
+
 // Bytes of the gradient's fp32 sums of split tiles.
-size_t split_bytes(int64_t rows, int64_t N, int64_t K) {
+size_t split_bytes(int64_t rows, int64_t N, int64_t K, bool distill) {
   if (rows <= 0) return 0;
-  if (rows <= kHeadFewTokens) return static_cast<size_t>(few_splits(N, K)) * rows * K * 4;
+  if (rows <= kHeadFewTokens)
+    return static_cast<size_t>(few_splits(N, K)) * (two_parts(rows, distill) ? 2 * rows : rows) * K * 4;
   const HeadGrid d = grad_grid(rows, N, K);
   return static_cast<size_t>(d.ntail) * d.nsplit * d.tn * TM * 4;
 }
@@ -1036,8 +1045,9 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
   }
   if (grad) {
     s.rscale = static_cast<float4*>(take(static_cast<size_t>(rows) * 16));
-    s.e = static_cast<uint16_t*>(take(static_cast<size_t>(rows) * e_pitch(N) * 2));
-    s.split = static_cast<float*>(take(std::max(split_bytes(rows, N, K), split_bytes(last, N, K))));
+    // (a last piece that is stored in two parts is shorter than half of the others)
+    s.e = static_cast<uint16_t*>(take(static_cast<size_t>(two_parts(rows, distill) ? 2 * rows : rows) * e_pitch(N) * 2));
+    s.split = static_cast<float*>(take(std::max(split_bytes(rows, N, K, distill), split_bytes(last, N, K, distill))));
   }
   s.bytes = at;
   return s;
@@ -1121,6 +1131,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     p.c = 1.4426950408889634f / a.temperature;
     p.part = s.part;
     p.e = s.e;
+    p.e_low = grad && two_parts(rows, distill) ? s.e + rows * lde : nullptr;
     p.lde = lde;
     p.labels = distill ? nullptr : a.labels + r0;
     p.sidx = s.sidx;
@@ -1168,6 +1179,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     t.lse = a.lse + r0;
     t.rscale = s.rscale;
     t.e = s.e;
+    t.e_low = p.e_low;
     t.lde = lde;
     t.tn = seg.tn;
     t.sw = seg.sw;
@@ -1184,6 +1196,7 @@ cudaError_t launch_head_loss(const HeadArgs& a, cudaStream_t st) {
     q.W = h.W;
     q.out = a.dX + r0 * a.K;
     q.split = s.split;
+    q.two_parts = p.e_low != nullptr;
     if (few) {
       err = launch_few_grad(h, s.e, lde, few_splits(a.N, a.K), q, st);
       if (err != cudaSuccess) return err;

@@ -8,6 +8,15 @@ namespace qn {
 
 constexpr float kHeadFits = 64.0f;  // |reference| (log2) up to which e is stored without it
 constexpr int kHeadFewTokens = 128;
+// Tokens up to which a teacher's p - q are stored in two parts, the bf16 value and
+// what its rounding left (in rows of its own behind the tokens'): the values of one
+// token often share a mantissa (a flat teacher's are all near -1 / k), so that their
+// roundings add up instead of cancelling.  dX of single tokens at T = 4: error 2.6e-3
+// with one part, 1.7e-3 (its own rounding to bf16) with two.  Over many tokens the
+// roundings differ (at most 2.2e-3 with one part), and the second part costs the more
+// the wider the products get: 32000 x 4096, 64 slots, one / two parts: 16 tokens 105 /
+// 106 us (NF4 head 95 / 100), 32 tokens 108 / 115 us.
+constexpr int kHeadTwoParts = 16;
 
 // The frozen head: W, or (W null) the NF4 weight.
 struct HeadWeight {
@@ -43,6 +52,7 @@ struct HeadEpi {
   float c;                   // log2(e) / T
   float2* part;              // [segments][rows], per column segment: (reference n, sum of exp2(z c - n))
   uint16_t* e;               // [rows][lde] (nullable)
+  uint16_t* e_low;           // few tokens: [rows][lde] to be written as zeros (nullable)
   int64_t lde;
   const int64_t* labels;     // [rows] (cross entropy), or
   const int* sidx;           // [rows][k] targets in ascending order, and
@@ -56,6 +66,7 @@ struct HeadEpi {
   const uint16_t* W;         // both modes: bf16 head (few tokens on an NF4 head: null)
   uint16_t* out;             // [rows][cols]
   float* split;              // fp32 sums of the split tiles' pieces
+  bool two_parts;            // few tokens: the sums of row i have a second part in row rows + i
 };
 
 // exp2 on the special-function unit: relative error about 2^-22, which is far

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 4);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nitems = g.tiles * g.nsplit, tokens = p.rows;
+  const int nitems = g.tiles * g.nsplit, tokens = MODE == 1 && p.two_parts ? 2 * p.rows : p.rows;
 
   // Item i: piece z of tile nt; pieces of one range of the contraction follow
   // one another, so the CTAs walk it together.
@@ -392,9 +392,13 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
               if (c0 < ewidth)  // groups of four entries are whole: br % 8 == 0, lde % 64 == 0
                 *reinterpret_cast<uint2*>(er + c0) = make_uint2(bf16x2_bits(e[u][0] * back, e[u][1] * back),
                                                                 bf16x2_bits(e[u][2] * back, e[u][3] * back));
+              uint16_t* el = p.e_low ? p.e_low + static_cast<int64_t>(row) * p.lde + v0 : nullptr;
+              if (el && c0 < ewidth) *reinterpret_cast<uint2*>(el + c0) = make_uint2(0u, 0u);
               if (nt == g.tiles - 1)  // the pitch may reach past the last tile
-                for (int64_t c = v0 + g.br + c0; c < p.lde; c += 128)
-                  *reinterpret_cast<uint2*>(er + (c - v0)) = make_uint2(0u, 0u);
+                for (int64_t c = g.br + c0; c < p.lde - v0; c += 128) {
+                  *reinterpret_cast<uint2*>(er + c) = make_uint2(0u, 0u);
+                  if (el) *reinterpret_cast<uint2*>(el + c) = make_uint2(0u, 0u);
+                }
             }
             if (!p.labels) {
               const uint16_t* o = p.off + static_cast<int64_t>(row) * (g.tiles + 1) + nt;
@@ -558,12 +562,22 @@ __global__ void __launch_bounds__(128) k_few_join(const float* __restrict__ spli
   pdl_wait();  // the call's last kernel: it lets nothing start early (see k_head)
   const int c = (blockIdx.x * 128 + threadIdx.x) * 4, row = blockIdx.y;
   if (c >= p.cols) return;
-  const int64_t at = static_cast<int64_t>(row) * p.cols + c, piece = static_cast<int64_t>(p.rows) * p.cols;
+  const int64_t at = static_cast<int64_t>(row) * p.cols + c, part = static_cast<int64_t>(p.rows) * p.cols;
+  const int64_t piece = p.two_parts ? 2 * part : part;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
   for (int z = 0; z < nsplit; ++z) {
     const float4 x = *reinterpret_cast<const float4*>(split + at + z * piece);
     a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+  }
+  if (p.two_parts) {
+    float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int z = 0; z < nsplit; ++z) {
+      const float4 x = *reinterpret_cast<const float4*>(split + at + part + z * piece);
+      b.x += x.x; b.y += x.y; b.z += x.z; b.w += x.w;
+    }
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
   }
   const float4 f = p.rscale[row];
   const int label = __float_as_int(f.w);
@@ -703,14 +717,15 @@ cudaError_t launch_few_logits(const HeadWeight& h, const uint16_t* X, int br, co
 
 cudaError_t launch_few_grad(const HeadWeight& h, const uint16_t* P, int64_t ldp, int nsplit, const HeadEpi& p,
                             cudaStream_t st) {
-  FewGrid g = few_grid(p.rows, 0, !h.W);
+  const int64_t rows = p.two_parts ? 2 * p.rows : p.rows;
+  FewGrid g = few_grid(rows, 0, !h.W);
   g.br = UM;
   g.tiles = static_cast<int>((h.K + UM - 1) / UM);
   g.nsplit = nsplit;
   g.numK = static_cast<int>((h.N + SUB * BK - 1) / (SUB * BK));
   CUtensorMap w{}, x;
   if ((h.W && !make_map(&w, BF16, h.W, h.K, h.N, h.K * 2, 64, BK, SW128)) ||
-      !make_map(&x, BF16, P, ldp, p.rows, ldp * 2, BK, p.rows, SW128)) return cudaErrorInvalidValue;
+      !make_map(&x, BF16, P, ldp, rows, ldp * 2, BK, rows, SW128)) return cudaErrorInvalidValue;
   const int lg = block_log2(h.block);
   cudaError_t e = launch_few<1>(w, x, g, p, h, st);
   if (e != cudaSuccess) return e;

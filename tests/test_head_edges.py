@@ -480,3 +480,42 @@ def test_contraction_in_rounds(L, M, N, K, nf4):
     compare(qb.qlora_head_distill(head, X, idx, t, 2.0, dloss=dloss),
             reference(values, X, 2.0, *distill_targets(idx, t, N, 2.0), dloss))
     assert qb.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M", [1, 7, 15, 16])
+@pytest.mark.parametrize("k", [3, 40, 200])
+def test_gradient_of_a_flat_teacher(L, M, k, nf4):
+    """Slots of one weight share a mantissa, so their p - q would round the same way: a token's dX off by up to 2^-9 of
+    itself beside its own rounding.  Held to that rounding alone: at most 2^-9 of every value, so of a token's norm;
+    the p of entries that are no slots round one by one, an error of 2^-9 sqrt(sum p^2) beside a gradient of
+    sqrt(k) / k times a row of W, and the fp32 sums are far below: together under a sixth of 2^-9 here."""
+    N, K, T = 20000, 512, 4.0
+    head, values, X, _, g = make(M + k, M, N, K, 64 if nf4 else 0, w_std=0.02)
+    idx = torch.stack([torch.randperm(N, generator=g)[:k] for _ in range(M)]).cuda()
+    t = torch.full((M, k), 1.0, device="cuda")
+    dloss = torch.rand(M, generator=g).cuda() + 0.5
+    loss, lse, dx = qb.qlora_head_distill(head, X, idx, t, T, dloss=dloss)
+    targets = distill_targets(idx, t, N, T)
+    ref = reference(values, X, T, *targets, dloss)
+    compare((loss, lse, dx), ref)
+    p = torch.softmax(X.double() @ values.double().T / T, 1)
+    assert (p.square().sum(1).sqrt() < k**-0.5 / 6).all()
+    rel = (dx.double() - ref["dx"]).norm(dim=1) / ref["dx"].norm(dim=1)
+    assert (rel <= 2.0**-9 * (1 + 1 / 6)).all(), rel.max()
+
+
+@gpu
+@pytest.mark.parametrize("M", [271, 272, 273, 513])
+def test_last_piece_in_two_parts(L, M):
+    """Pieces of 256 tokens and a last one of 1 to 17, in a workspace of exactly the size that the query returns."""
+    for N, K, k in ((1000, 192, 5), (4097, 512, 30)):
+        head, values, X, _, g = make(M + N, M, N, K)
+        idx, t = teacher(g, M, N, k, False)
+        dloss = torch.rand(M, generator=g).cuda()
+        nbytes = qb.head_workspace_bytes(M, N, K, k, piece=256)
+        ws = of_bytes(nbytes, 255)
+        got = qb.qlora_head_distill(head, X, idx, t, 2.0, dloss=dloss, workspace=ws[:nbytes])
+        compare(got, reference(values, X, 2.0, *distill_targets(idx, t, N, 2.0), dloss))
+        assert (ws[nbytes:] == 171).all()
