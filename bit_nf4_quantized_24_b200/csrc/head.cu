@@ -942,7 +942,7 @@ HeadGrid grad_tiles(int64_t rows, int64_t N, int64_t K, int nh, double* cost) {
   // Split in S, the w tiles of the last wave take ceil(w S / P) rounds of S-ths;
   // their fp32 sums (256 KB per piece and accumulator, written and read again)
   // cost about 0.2 of a stage each, and every round the filling and emptying of
-  // the pipeline.
+  // the pipeline, about 8 (both are estimates).
   for (int64_t S = 2; w && S <= std::min<int64_t>(numK / 8, 64); ++S) {
     const double rounds = static_cast<double>((w * S + P - 1) / P);
     const double t = rounds / static_cast<double>(S) * static_cast<double>(numK) * stage +

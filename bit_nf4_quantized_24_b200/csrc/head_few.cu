@@ -28,8 +28,9 @@ constexpr int BUF_PITCH = UM + 4;     // floats per token in the epilogue's buff
 constexpr int BUF_TOKENS = 16;
 constexpr int BUF_BYTES = 2 * BUF_TOKENS * BUF_PITCH * 4;  // per set of epilogue warps
 // Sets of four epilogue warps, which take turns at 16 tokens: two on a bf16 head
-// (128 tokens, 8000 x 1024 / 32000 x 2048 with the gradient: 38 / 73 us with one set,
-// 32 / 66 us with two); an NF4 head's block has no threads to spare.
+// (128 tokens, 8000 x 1024 / 32000 x 2048 with the gradient, on the GPU: 38 / 73 us
+// with one set, 32 / 66 us with two; now 64 us); an NF4 head's block has no threads to
+// spare.
 __host__ __device__ constexpr int epi_sets(bool nf4) { return nf4 ? 1 : 2; }
 constexpr int BAR_BYTES = 512;
 constexpr int SMEM_MAX = 232448;
@@ -428,7 +429,8 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
     // two groups of 64 columns.  A thread expands one group of two rows, 16 apart,
     // its neighbour the other group: their codes are 64 contiguous bytes, and a load
     // touches 16 rows (a load instruction costs a cycle per 128-byte line; 16 tokens
-    // on a 32000 x 4096 head with the gradient: 108 us, with a row per lane 117).
+    // on a 32000 x 4096 head with the gradient, when this was chosen: 108 us, with a
+    // row per lane 117; now 90 us).
     const int row0 = (e & 3) * 32 + (lane >> 1), half = lane & 1;
     struct Walk {
       int i, nt, z, k, kend;
@@ -676,7 +678,8 @@ int few_tile_rows(int64_t N) {
   int best = UM;
   int64_t cost = 0;
   for (int br = UM; br >= 32; br -= 8) {
-    // a tile costs its rows, and its start and epilogue about what 16 rows cost
+    // a tile costs its rows, and its start and epilogue about what 16 rows cost (an
+    // estimate, as is the 2 in few_splits)
     const int64_t c = ((N + br - 1) / br + P - 1) / P * (br + 16);
     if (br == UM || c < cost) {
       cost = c;

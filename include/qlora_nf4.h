@@ -371,20 +371,21 @@ int qlora_linear_fwd_noalloc(const uint8_t* codes, const uint8_t* absmax_q, cons
  * either (an entry of W that is not finite itself makes its column of dX NaN for
  * every token, as the sums above do).  With dX, N max |W| must stay below 2^63: W
  * is multiplied by exponentials of up to 2^64 before their sum is taken off.
- * Logits, statistics and sums are fp32 (loss and lse hold six digits: a relative
- * error of at most 1e-6 over a call's tokens).  p, and p - q at a teacher's slots,
+ * Logits, statistics and sums are fp32.  Over a call's tokens loss and lse hold
+ * about six digits (2-norm); a single token whose loss is a small difference of
+ * its logits is off by their fp32 rounding.  p, and p - q at a teacher's slots,
  * are rounded to bf16 before the second product, except a label's and a token's
  * largest p - q (fp32) and, in calls or last pieces of at most 16 tokens, the other
  * slots' (16 bits); dX is rounded once at the end.  Outputs must not overlap inputs.
  *
  * workspace: qlora_head_workspace bytes, 256-byte aligned.  Tokens are taken
  * in pieces; with a gradient the workspace holds M' x N bf16 values for a piece
- * of M' tokens (2 M' x N for a distillation of at most 16), without one some 8 to 20 bytes per 128 entries and token.  piece = 0
- * asks for the bytes of the library's own choice (at most 1 GB of either, or
- * what 256 tokens take, if that is more), another piece for at most that many
- * tokens at a time, in multiples of 256 (256 at least, or M, if fewer); the calls
- * use the largest such pieces that fit the workspace they get, and return
- * QLORA_ERR_WORKSPACE if none does.  k = 0 asks for qlora_head_xent, k >= 1 for
+ * of M' tokens (2 M' x N for a distillation of at most 16), without one some 8 to
+ * 20 bytes per 128 entries and token.  piece = 0 asks for the bytes of the
+ * library's own choice (at most 1 GB of either, or what 256 tokens take, if that
+ * is more), another piece for at most that many tokens at a time, in multiples of
+ * 256 (256 at least, or M, if fewer); the calls use the largest such pieces that
+ * fit the workspace they get, and return QLORA_ERR_WORKSPACE if none does.  k = 0 asks for qlora_head_xent, k >= 1 for
  * qlora_head_distill with k slots; want_dx: dX is not NULL; nf4: an NF4 head.
  * Results do not depend on other work of the device, and repeat bit for bit
  * with the same workspace size.
