@@ -11,8 +11,8 @@
 // The logits never reach memory.  A product kernel (k_head<0>) leaves, for each
 // row and each column segment of its tiles, a reference near the segment's
 // maximum and the sum of exponentials relative to it, and the logits of the
-// teacher's slots it meets, all in fp32 straight from the accumulator; k_head_stats joins them into
-// lse and loss.  For the gradient the same kernel also writes e = exp(z) in bf16
+// teacher's slots it meets, all in fp32 straight from the accumulator; k_head_stats
+// joins them into lse and loss.  For the gradient the same kernel also writes e = exp(z) in bf16
 // for a piece of the tokens, and k_head<1> multiplies e by W once lse is known:
 // p = e exp(-lse) is a factor of the whole row, so it waits for the epilogue,
 // and only the target columns of e change in between, because p - q from a rounded
@@ -641,12 +641,14 @@ struct RowStat {
 };
 
 // Writes p - q, relative to reference r, into the columns of the row's teacher
-// slots (one warp per row; what the rounding leaves into el, if given), all but the largest one: that one stays in fp32 (*d, and
-// its entry as the result) and is added in the gradient's epilogue as a label's is.
+// slots (one warp per row; what the rounding leaves into el, if given), all but the
+// largest one: that one stays in fp32 (*d, and its entry as the result) and is added
+// in the gradient's epilogue as a label's is.
 // (The slots' rounding to bf16 alone makes the error of dX 1.4 times that of a bf16
 // result, and the largest slot has most of it.)
-__device__ __forceinline__ int write_targets(uint16_t* er, uint16_t* el, const RowStat& st, int lane, int row, const int* sidx,
-                                             const float* logq, int k, const float2* ztgt, float* d_out) {
+__device__ __forceinline__ int write_targets(uint16_t* er, uint16_t* el, const RowStat& st, int lane, int row,
+                                             const int* sidx, const float* logq, int k, const float2* ztgt,
+                                             float* d_out) {
   const float up = exp2f((st.m - st.r) + st.l2s);
   const int64_t at = static_cast<int64_t>(row) * k;
   float best = 0.0f;
@@ -817,7 +819,9 @@ __global__ void __launch_bounds__(STAT_THREADS) k_head_stats(const __grid_consta
   const float g = any ? (p.dloss ? p.dloss[row] : 1.0f) * p.temp : 0.0f;
   if (p.e && g != 0.0f) {  // otherwise the row's gradient is written as zeros
     if (big) rescale_row(p, row, st.r, a);
-    if (!p.labels) label = write_targets(p.e + row * p.lde, p.e_low ? p.e_low + row * p.lde : nullptr, st, a, row, p.sidx, p.logq, p.k, p.ztgt, &d);
+    if (!p.labels)
+      label = write_targets(p.e + row * p.lde, p.e_low ? p.e_low + row * p.lde : nullptr, st, a, row, p.sidx, p.logq,
+                            p.k, p.ztgt, &d);
   }
   if (a == 0) {
     p.loss[row] = any ? total * (p.temp * p.temp) : 0.0f;
@@ -1046,7 +1050,8 @@ HeadSpace head_space(void* ws, int64_t rows, int64_t M, int64_t N, int64_t K, in
   if (grad) {
     s.rscale = static_cast<float4*>(take(static_cast<size_t>(rows) * 16));
     // (a last piece that is stored in two parts is shorter than half of the others)
-    s.e = static_cast<uint16_t*>(take(static_cast<size_t>(two_parts(rows, distill) ? 2 * rows : rows) * e_pitch(N) * 2));
+    const size_t e_rows = two_parts(rows, distill) ? 2 * rows : rows;
+    s.e = static_cast<uint16_t*>(take(e_rows * e_pitch(N) * 2));
     s.split = static_cast<float*>(take(std::max(split_bytes(rows, N, K, distill), split_bytes(last, N, K, distill))));
   }
   s.bytes = at;

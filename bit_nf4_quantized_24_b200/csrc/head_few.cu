@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(threads_of(KIND > 0), 1)
             for (int q = 0; q < 4; ++q) w[q] = ldg_nc_v4(p.W + at + 8 * q);
           } else {
             const uint4 c = ldg_nc_v4(codes + at / 2);
-            const float scale = dq ? __fmul_rn(static_cast<float>(absmax_q[blk]), dq_scale[blk >> 8]) : dq_scale[blk];
-            const Nf4Lut lut = make_lut(lv, scale);
+            const Nf4Lut lut = make_lut(
+                lv, dq ? __fmul_rn(static_cast<float>(absmax_q[blk]), dq_scale[blk >> 8]) : dq_scale[blk]);
             deq8(c.x, lut, w[0].x, w[0].y, w[0].z, w[0].w);
             deq8(c.y, lut, w[1].x, w[1].y, w[1].z, w[1].w);
             deq8(c.z, lut, w[2].x, w[2].y, w[2].z, w[2].w);
